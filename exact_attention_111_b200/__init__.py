@@ -5,10 +5,20 @@ kernels behind the C ABI of ``include/fa.h``.  The C entry points are mirrored o
 (``fa_fwd``, ``fa_bwd``, ``fa_fwd_ex``, ``fa_bwd_ex``, ``fa_bwd_workspace_bytes``,
 ``fa_bwd_workspace_bytes_ex``, ``fa_bwd_workspace_bytes_split``, ``fa_bwd_splitq_choose``, ``fa_bwd_noalloc``, ``fa_fwd_partial``, ``fa_lse_merge``, ``fa_fwd_splitkv``,
 ``fa_fwd_splitkv_workspace_bytes``, ``fa_splitkv_choose``, ``fa_fwd_fp8``, ``fa_fwd_fp8_workspace_bytes``, ``fa_selftest_wait_timeout``, ``fa_selftest_exp2_poly``, ``fa_check_status``,
+``fa_cache_append``, ``fa_cache_read``, ``fa_cache_keep``, ``fa_fwd_tree``, ``fa_fwd_tree_workspace_bytes``,
 ``fa_status_string``, ``fa_last_launch_count``); they take torch tensors (or raw device
 addresses as ints).  ``attention_forward`` / ``attention_backward`` /
 ``attention_forward_splitkv`` / ``attention_forward_partial`` / ``lse_merge`` and
 ``FlashAttention`` add output allocation with torch on top.
+
+Serving: ``KVCache`` describes a paged key/value cache (16-bit, or E4M3 quantised as it is
+written); ``cache_append`` writes new tokens' rows, ``attention_forward_tree`` lets the new tokens (one, a
+chain, or a tree of drafted tokens, ``tree_mask``) attend over it, ``cache_keep`` keeps the accepted
+ones, ``cache_read`` reads it back as dense tensors:
+
+    cache_append(cache, k, v, cu, lens)
+    o, lse = attention_forward_tree(q, cache, cu, lens, max_new, tree_mask=tree_mask(parents, cu))
+    cache_keep(cache, lens, kept, counts);  lens += counts
 
 There is no fallback: if ``libfa.so`` is missing or a call fails, an exception is raised.
 """
@@ -26,10 +36,12 @@ __all__ = [
     "fa_splitkv_choose", "attention_forward_splitkv", "attention_forward_partial", "lse_merge",
     "FA_MAX_PARTS", "fa_bwd_workspace_bytes_ex", "fa_bwd_workspace_bytes_split", "fa_bwd_splitq_choose", "FA_ERR_RANGE", "fa_fwd_fp8", "fa_fwd_fp8_workspace_bytes",
     "attention_forward_fp8", "fa_selftest_wait_timeout", "fa_selftest_exp2_poly",
+    "FA_E4M3", "KVCache", "fa_cache_append", "fa_cache_read", "fa_cache_keep", "fa_fwd_tree",
+    "fa_fwd_tree_workspace_bytes", "cache_append", "cache_read", "cache_keep", "attention_forward_tree", "tree_mask",
 ]
 
 FA_OK, FA_ERR_INVALID_ARG, FA_ERR_UNSUPPORTED, FA_ERR_CUDA, FA_ERR_TIMEOUT, FA_ERR_WORKSPACE, FA_ERR_RANGE = range(7)
-FA_BF16, FA_FP16, FA_FP32 = 0, 1, 2
+FA_BF16, FA_FP16, FA_FP32, FA_E4M3 = 0, 1, 2, 3
 TILE = 128
 FA_MAX_PARTS = 64
 
@@ -40,6 +52,7 @@ _lib = None
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
+_ll = ctypes.c_longlong
 
 
 class FwdArgs(ctypes.Structure):
@@ -74,6 +87,40 @@ class Fp8Args(ctypes.Structure):
                 ("o", _vp), ("lse", _vp), ("B", _i), ("H", _i), ("N", _i), ("d", _i), ("scale", _f),
                 ("causal", _i), ("blockmask", _vp), ("o_fp32", _i), ("workspace", _vp),
                 ("workspace_bytes", ctypes.c_size_t), ("stream", _vp)]
+
+
+class CacheArgs(ctypes.Structure):
+    """Mirror of fa_cache."""
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("page_table", _vp),
+                ("pages", _i), ("Hk", _i), ("page_size", _i), ("d", _i), ("dtype", _i),
+                ("B", _i), ("max_pages", _i), ("table_stride", _i)]
+
+
+class CacheAppendArgs(ctypes.Structure):
+    """Mirror of fa_cache_append_args."""
+    _fields_ = [("cache", CacheArgs), ("k_new", _vp), ("v_new", _vp),
+                ("k_token_stride", _ll), ("k_head_stride", _ll), ("v_token_stride", _ll), ("v_head_stride", _ll),
+                ("cu_new", _vp), ("lens", _vp), ("total", _i), ("dtype", _i), ("stream", _vp)]
+
+
+class CacheReadArgs(ctypes.Structure):
+    """Mirror of fa_cache_read_args."""
+    _fields_ = [("cache", CacheArgs), ("lens", _vp), ("k_out", _vp), ("v_out", _vp), ("N", _i), ("dtype", _i),
+                ("stream", _vp)]
+
+
+class CacheKeepArgs(ctypes.Structure):
+    """Mirror of fa_cache_keep_args."""
+    _fields_ = [("cache", CacheArgs), ("lens", _vp), ("kept", _vp), ("counts", _vp), ("width", _i), ("stream", _vp)]
+
+
+class TreeArgs(ctypes.Structure):
+    """Mirror of fa_fwd_tree_args."""
+    _fields_ = [("cache", CacheArgs), ("q", _vp), ("o", _vp), ("lse", _vp),
+                ("q_token_stride", _ll), ("q_head_stride", _ll), ("o_token_stride", _ll), ("o_head_stride", _ll),
+                ("cu_new", _vp), ("lens", _vp), ("tree_mask", _vp), ("mask_words", _i),
+                ("total", _i), ("Hq", _i), ("max_new", _i), ("dtype", _i), ("scale", _f),
+                ("workspace", _vp), ("workspace_bytes", ctypes.c_size_t), ("stream", _vp)]
 
 
 class FAError(RuntimeError):
@@ -132,6 +179,16 @@ def lib() -> ctypes.CDLL:
     L.fa_selftest_wait_timeout.restype = _i
     L.fa_selftest_exp2_poly.argtypes = [_vp, _vp, _i, _vp]
     L.fa_selftest_exp2_poly.restype = _i
+    L.fa_cache_append.argtypes = [ctypes.POINTER(CacheAppendArgs)]
+    L.fa_cache_append.restype = _i
+    L.fa_cache_read.argtypes = [ctypes.POINTER(CacheReadArgs)]
+    L.fa_cache_read.restype = _i
+    L.fa_cache_keep.argtypes = [ctypes.POINTER(CacheKeepArgs)]
+    L.fa_cache_keep.restype = _i
+    L.fa_fwd_tree.argtypes = [ctypes.POINTER(TreeArgs)]
+    L.fa_fwd_tree.restype = _i
+    L.fa_fwd_tree_workspace_bytes.argtypes = [_i, _i, _i, _i]
+    L.fa_fwd_tree_workspace_bytes.restype = ctypes.c_size_t
     _lib = L
     return L
 
@@ -270,6 +327,36 @@ def fa_fwd_fp8(q8, k8, v8, descale_q, descale_k, descale_v, o, lse, B, H, N, d, 
                 _ptr(lse), B, H, N, d, scale, int(bool(causal)), _ptr(blockmask), int(bool(o_fp32)),
                 _ptr(workspace), workspace_bytes, _stream(stream))
     _check(lib().fa_fwd_fp8(ctypes.byref(a)), "fa_fwd_fp8")
+
+
+def fa_cache_append(cache, k_new, v_new, k_strides, v_strides, cu_new, lens, total, dtype, stream=None):
+    """cache: a CacheArgs; strides: (token, head) in elements."""
+    a = CacheAppendArgs(cache, _ptr(k_new), _ptr(v_new), *k_strides, *v_strides, _ptr(cu_new), _ptr(lens), total,
+                        dtype, _stream(stream))
+    _check(lib().fa_cache_append(ctypes.byref(a)), "fa_cache_append")
+
+
+def fa_cache_read(cache, lens, k_out, v_out, N, dtype, stream=None):
+    a = CacheReadArgs(cache, _ptr(lens), _ptr(k_out), _ptr(v_out), N, dtype, _stream(stream))
+    _check(lib().fa_cache_read(ctypes.byref(a)), "fa_cache_read")
+
+
+def fa_cache_keep(cache, lens, kept, counts, width, stream=None):
+    a = CacheKeepArgs(cache, _ptr(lens), _ptr(kept), _ptr(counts), width, _stream(stream))
+    _check(lib().fa_cache_keep(ctypes.byref(a)), "fa_cache_keep")
+
+
+def fa_fwd_tree_workspace_bytes(total: int, Hq: int, Hk: int, d: int) -> int:
+    return lib().fa_fwd_tree_workspace_bytes(total, Hq, Hk, d)
+
+
+def fa_fwd_tree(cache, q, o, lse, q_strides, o_strides, cu_new, lens, tree_mask, mask_words, total, Hq, max_new,
+                dtype, scale, workspace, workspace_bytes, stream=None):
+    """cache: a CacheArgs; strides: (token, head) in elements."""
+    a = TreeArgs(cache, _ptr(q), _ptr(o), _ptr(lse), *q_strides, *o_strides, _ptr(cu_new), _ptr(lens),
+                 _ptr(tree_mask), mask_words, total, Hq, max_new, dtype, scale, _ptr(workspace), workspace_bytes,
+                 _stream(stream))
+    _check(lib().fa_fwd_tree(ctypes.byref(a)), "fa_fwd_tree")
 
 
 def _event(e):
@@ -417,6 +504,177 @@ def attention_backward(q, k, v, o, lse, dout, causal=False, blockmask=None, scal
               _dtype_code(q), visit_log, workspace, workspace.numel(), stream, deterministic=deterministic,
               dropout_p=dropout_p, dropout_seed=dropout_seed, query_splits=query_splits)
     return dq, dk, dv
+
+
+class KVCache:
+    """A paged key/value cache (fa_cache of include/fa.h): the caller's tensors and their checks.
+
+    ``k``, ``v``: [pages, Hk, page_size, d] CUDA tensors, contiguous, bf16 or fp16, or E4M3 codes
+    (torch.float8_e4m3fn or uint8) with ``k_scale``, ``v_scale`` [pages, Hk, page_size] E8M0 codes
+    (torch.float8_e8m0fnu or uint8).  ``page_table``: int32 [B, max_pages]; its contents may change
+    between calls.  The object keeps the tensors alive and allocates nothing."""
+
+    def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
+        import torch
+        for t in (k, v):
+            if not (t.is_cuda and t.is_contiguous() and t.dim() == 4 and t.shape == k.shape and t.dtype == k.dtype):
+                raise ValueError("expected k and v as contiguous CUDA tensors of one type, [pages, Hk, page_size, d]")
+        if k.element_size() == 1:
+            if k.dtype not in (torch.float8_e4m3fn, torch.uint8):
+                raise TypeError(f"unsupported cache dtype {k.dtype}")
+            for t in (k_scale, v_scale):
+                if t is None or not (t.is_cuda and t.is_contiguous() and t.element_size() == 1
+                                     and t.shape == k.shape[:3]):
+                    raise ValueError("an E4M3 cache needs k_scale and v_scale, [pages, Hk, page_size] E8M0 codes")
+            self.dtype = FA_E4M3
+        else:
+            if k_scale is not None or v_scale is not None:
+                raise ValueError("scales belong to an E4M3 cache")
+            self.dtype = _dtype_code(k)
+        if not (page_table.is_cuda and page_table.dtype == torch.int32 and page_table.dim() == 2
+                and (page_table.shape[1] == 1 or page_table.stride(1) == 1)):
+            raise ValueError("expected page_table as an int32 CUDA tensor [B, max_pages]")
+        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
+        self.device = k.device
+        for t in (v, k_scale, v_scale, page_table):
+            if t is not None and t.device != k.device:
+                raise ValueError("the cache's tensors are on different devices")
+        self.pages, self.Hk, self.page_size, self.d = k.shape
+        self.B, self.max_pages = page_table.shape
+        self.args = CacheArgs(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), self.pages, self.Hk,
+                              self.page_size, self.d, self.dtype, self.B, self.max_pages,
+                              page_table.stride(0) if self.B > 1 else max(self.max_pages, 1))
+
+    def _lengths(self, *named):
+        import torch
+        for name, t, n in named:
+            if not (t.device == self.device and t.dtype == torch.int32 and t.is_contiguous() and t.shape == n):
+                raise ValueError(f"expected {name} as a contiguous int32 tensor {list(n)} on the cache's device")
+
+    def _rows(self, name, t, heads):
+        """(token, head) strides of a [total, heads, d] tensor; heads None: any multiple of Hk."""
+        if not (t.device == self.device and t.dim() == 3 and t.shape[2] == self.d and t.stride(2) == 1
+                and (t.shape[1] == heads if heads is not None else t.shape[1] > 0 and t.shape[1] % self.Hk == 0)):
+            raise ValueError(f"expected {name} as [total, heads, {self.d}] on the cache's device, its last dimension contiguous")
+        return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+
+    def _type(self, t):
+        code = _dtype_code(t)
+        if self.dtype != FA_E4M3 and code != self.dtype:
+            raise TypeError(f"{t.dtype} tensors with a cache of {self.k.dtype}")
+        return code
+
+
+def _on_device(cache, call, *args):
+    """Run ``call`` with the cache's device current (CUDA launches go to the current device)."""
+    import torch
+    if cache.device.index == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(cache.device):
+        return call(*args)
+
+
+def cache_append(cache, k_new, v_new, cu_new, lens, stream=None):
+    """Write the rows of new tokens, k_new and v_new [total, Hk, d] (bf16 or fp16; strided views
+    will do), behind what each sequence holds (fa_cache_append): token cu_new[b] + i goes to position
+    lens[b] + i of sequence b.  ``lens`` is not changed.  An E4M3 cache quantises them."""
+    ks, vs = cache._rows("k_new", k_new, cache.Hk), cache._rows("v_new", v_new, cache.Hk)
+    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+        raise ValueError("k_new and v_new differ in shape or type")
+    cache._lengths(("cu_new", cu_new, (cache.B + 1,)), ("lens", lens, (cache.B,)))
+    _on_device(cache, fa_cache_append, cache.args, k_new, v_new, ks, vs, cu_new, lens, k_new.shape[0],
+               cache._type(k_new), stream)
+
+
+def cache_read(cache, lens, N, dtype=None, k_out=None, v_out=None, stream=None):
+    """The cache as dense (K, V), [B, Hk, N, d] 16-bit tensors with zeros past lens[b]
+    (fa_cache_read).  ``dtype``: of an E4M3 cache's result, torch.bfloat16 (default) or float16;
+    ``k_out``, ``v_out``: tensors to write to."""
+    import torch
+    cache._lengths(("lens", lens, (cache.B,)))
+    shape = (cache.B, cache.Hk, N, cache.d)
+    if dtype is None:
+        dtype = k_out.dtype if k_out is not None else torch.bfloat16 if cache.dtype == FA_E4M3 else cache.k.dtype
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
+    for t in (k_out, v_out):
+        if not (t.device == cache.device and t.shape == shape and t.is_contiguous() and t.dtype == dtype):
+            raise ValueError(f"expected k_out and v_out as contiguous {dtype} tensors {list(shape)}")
+    _on_device(cache, fa_cache_read, cache.args, lens, k_out, v_out, N, cache._type(k_out), stream)
+    return k_out, v_out
+
+
+def cache_keep(cache, lens, kept, counts, stream=None):
+    """Keep accepted rows of drafted tokens (fa_cache_keep): row lens[b] + kept[b, i] moves to row
+    lens[b] + i, i < counts[b].  ``kept`` int32 [B, width], strictly increasing along a row; ``counts``
+    int32 [B].  ``lens`` is not changed."""
+    if kept.dim() != 2:
+        raise ValueError("expected kept as [B, width]")
+    cache._lengths(("lens", lens, (cache.B,)), ("kept", kept, (cache.B, kept.shape[1])), ("counts", counts, (cache.B,)))
+    _on_device(cache, fa_cache_keep, cache.args, lens, kept, counts, kept.shape[1], stream)
+
+
+def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scale=None, workspace=None, o=None,
+                           lse=None, stream=None):
+    """Attention of new tokens q [total, Hq, d] over the cache that already holds their rows
+    (fa_fwd_tree).  ``tree_mask``: None for a chain (token t sees new tokens j <= t), or int64
+    [total, words] visibility bits (see ``tree_mask``).  ``max_new``: at least every sequence's number of
+    new tokens.  ``o``, ``lse``, ``workspace``: tensors to use instead of new ones.  Returns (O, LSE),
+    [total, Hq, d] and fp32 [total, Hq]."""
+    import torch
+    qs = cache._rows("q", q, None)
+    code = cache._type(q)
+    total, Hq, d = q.shape
+    cache._lengths(("cu_new", cu_new, (cache.B + 1,)), ("lens", lens, (cache.B,)))
+    words = 0
+    if tree_mask is not None:
+        if not (tree_mask.device == cache.device and tree_mask.dtype == torch.int64 and tree_mask.dim() == 2
+                and tree_mask.is_contiguous() and tree_mask.shape[0] == total):
+            raise ValueError("expected tree_mask as a contiguous int64 tensor [total, words] on the cache's device")
+        words = tree_mask.shape[1]
+    if o is None:
+        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif o.shape != q.shape or o.dtype != q.dtype:
+        raise ValueError("o and q differ in shape or type")
+    os_ = cache._rows("o", o, Hq)
+    if lse is None:
+        lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
+    elif not (lse.device == cache.device and lse.dtype == torch.float32 and lse.shape == (total, Hq)
+              and lse.is_contiguous()):
+        raise ValueError("expected lse as a contiguous float32 tensor [total, Hq]")
+    if workspace is None:
+        workspace = torch.empty(fa_fwd_tree_workspace_bytes(total, Hq, cache.Hk, d), dtype=torch.uint8, device=q.device)
+    elif not (workspace.device == cache.device and workspace.is_contiguous()):
+        raise ValueError("expected workspace as a contiguous tensor on the cache's device")
+    _on_device(cache, fa_fwd_tree, cache.args, q, o, lse, qs, os_, cu_new, lens, tree_mask, words, total, Hq,
+               int(max_new), code, 1.0 / d ** 0.5 if scale is None else scale, workspace,
+               workspace.numel() * workspace.element_size(), stream)
+    return o, lse
+
+
+def tree_mask(parents, cu_new, words=None):
+    """Visibility bits of drafted trees: int64 [total, words] with bit j of token t's row set iff new
+    token j of its sequence is t itself or one of its ancestors.  ``parents``: int [total], the
+    parent's index within the sequence's new tokens, smaller than the token's own, or -1 (only the prefix above
+    it); ``cu_new`` as for attention_forward_tree.  Computed on the host (trees are
+    drafted there or are fixed); the result is on ``cu_new``'s device."""
+    import torch
+    par, cu = [int(x) for x in parents], [int(x) for x in cu_new]
+    most = max([b - a for a, b in zip(cu, cu[1:])] + [1])
+    words = (most + 63) // 64 if words is None else words
+    if 64 * words < most:
+        raise ValueError(f"{words} words hold no {most} tokens")
+    rows = [0] * len(par)
+    for a, b in zip(cu, cu[1:]):
+        for t in range(a, b):
+            if not -1 <= par[t] < t - a:
+                raise ValueError(f"token {t - a}'s parent {par[t]} does not precede it")
+            rows[t] = (rows[a + par[t]] if par[t] >= 0 else 0) | 1 << (t - a)
+    full = (1 << 64) - 1
+    vals = [[((r >> 64 * w & full) ^ 1 << 63) - (1 << 63) for w in range(words)] for r in rows]
+    return torch.tensor(vals, dtype=torch.int64, device=cu_new.device).reshape(len(par), words)
 
 
 def _make_autograd():

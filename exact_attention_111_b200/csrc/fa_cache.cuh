@@ -1,0 +1,252 @@
+// fa_cache.cuh -- the paged key/value cache as the kernels see it: slot addressing, the E4M3 row
+// format (quantise, expand), and the schedule of the attention over the cache, shared by its
+// kernels.  Not part of the public ABI.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fa.h"
+#include "fa_internal.h"
+
+namespace fa {
+
+// K and V pages [pages][Hk][page_size][d], E8M0 scale codes [pages][Hk][page_size] (E4M3 only).
+struct CacheView {
+  uint8_t* k;
+  uint8_t* v;
+  uint8_t* ks;
+  uint8_t* vs;
+  const int* table;      // [B, max_pages], rows table_stride apart
+  int* status;           // device status word
+  int pages, Hk, d, B, max_pages, table_stride;
+  int page_shift;        // log2(page_size)
+};
+
+// Records a page id, length or index that the cache cannot hold; the first error wins.
+__device__ __forceinline__ void flag_range(const CacheView& c) { atomicCAS(c.status, 0, kDevRange); }
+
+// Row index (page * Hk + h) * page_size + r of key position pos of sequence b, or -1 (flagged)
+// when the position lies past the table or its page id is no page.
+__device__ __forceinline__ long long slot_row(const CacheView& c, int b, int h, long long pos) {
+  const long long e = pos >> c.page_shift;
+  if (pos < 0 || e >= c.max_pages) {
+    flag_range(c);
+    return -1;
+  }
+  const int p = c.table[(long long)b * c.table_stride + e];
+  if (p < 0 || p >= c.pages) {
+    flag_range(c);
+    return -1;
+  }
+  return (((long long)p * c.Hk + h) << c.page_shift) + (pos & ((1 << c.page_shift) - 1));
+}
+
+// The sequence that owns token tok: the last b with cu[b] <= tok < cu[b + 1], or -1.  One warp
+// searches 32-ary: 2 rounds of independent loads up to 1024 sequences.
+__device__ __forceinline__ int owner_of(const int* cu, int B, int tok) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0, n = B + 1;                 // count of entries cu[lo .. lo + n) <= tok, over cu[0 .. B]
+  while (n > 0) {
+    const int step = (n + 31) >> 5;
+    const int i = lo + (lane + 1) * step - 1;
+    const bool le = (lane + 1) * step <= n && cu[i] <= tok;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    lo += c * step;
+    n = min(step - 1, n - c * step);
+  }
+  return lo >= 1 && lo <= B ? lo - 1 : -1;
+}
+
+// ------------------------------------------------------------------------------------
+// E4M3 rows.  A row of d values x is stored as codes and one power-of-two scale 2^e, with e the
+// smallest exponent for which max |x| <= 448 * 2^e: the largest magnitude lands in (224, 448], the
+// codes are x * 2^-e (an exact product) rounded to nearest even, and code * 2^e is exact in
+// bf16, so reading back adds no error.  A power of two costs no precision against max/448: E4M3
+// is a floating type, so a factor below 2 moves no value out of its normal range but the lowest binade.
+// ------------------------------------------------------------------------------------
+
+// E8M0 code e + 127 of a row whose largest finite magnitude is amax: with amax = 2^(E-127) (1 + M),
+// e = E - 127 - 8, one more when 1 + M > 1.75 (448 = 1.75 * 2^8).
+__device__ __forceinline__ int scale_code(float amax) {
+  const uint32_t u = __float_as_uint(amax);
+  const int s = static_cast<int>(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+  return max(s, 1);                      // at most 254 - 8 + 1 = 247
+}
+__device__ __forceinline__ float scale_value(uint32_t code) { return __uint_as_float(code << 23); }   // 2^(code - 127)
+__device__ __forceinline__ float scale_inverse(int code) { return __uint_as_float((254u - code) << 23); }
+
+// Two fp32 to two E4M3 codes (lo = first), round to nearest even; NaN gives the NaN code.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+// Two E4M3 codes (low 16 bits) to two fp16, exact.
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t w) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(r) : "r"(w));
+  return r;
+}
+
+// ------------------------------------------------------------------------------------
+// Schedule of the attention over the cache.  A unit is one (sequence, key head, row tile): rows are
+// the unit's (new token, query head of the group) pairs.  Its keys are cut into chunks of 128.
+// All chunks of all units stand in one line -- sequences, in them key heads, in them row tiles,
+// in them chunks -- and CTA c of C takes the c-th of C equal parts, whatever units it cuts.
+// Every warp finds its part from the lengths on the device, so the host needs none of them.
+// ------------------------------------------------------------------------------------
+
+constexpr int kChunk = 128;      // keys
+constexpr int kTreeCtas = 148;   // most CTAs (one per SM)
+
+struct TreeArgs {
+  CacheView c;
+  const uint16_t* q;             // [total, Hq, d], strides below
+  uint16_t* o;                   // [total, Hq, d]
+  float* lse;                    // [total, Hq], dense
+  const int* cu;                 // [B + 1]
+  const int* lens;               // [B]
+  const unsigned long long* mask;   // [total, words] or null
+  float* part_o;                 // [C, 2, tile_rows, d] partial sums of units cut between CTAs
+  float* part_ml;                // [C, 2, tile_rows, 2] their running max (log2 units) and sum
+  int4* meta;                    // [C] what CTA c leaves to the merge
+  long long q_tok, q_head, o_tok, o_head;   // strides in elements
+  int total, Hq, G, words, max_new;
+  int tile_rows;                 // rows of a row tile (a multiple of G tokens' rows or of 16)
+  unsigned long long timeout_ns;
+  float scale_log2;
+};
+
+// One sequence's numbers.
+struct SeqView {
+  int T, len, cu0;               // new tokens, prefix keys, first token
+  int RT, KT;                    // row tiles per key head, chunks
+};
+
+// Reads sequence b; T = 0 where there is nothing to do or (flagged) the lengths cannot be.
+__device__ __forceinline__ SeqView load_seq(const TreeArgs& a, int b, bool flag) {
+  SeqView s{0, 0, 0, 0, 0};
+  const int c0 = a.cu[b], c1 = a.cu[b + 1], len = a.lens[b];
+  const long long T = (long long)c1 - c0, L = (long long)len + T;
+  if (T == 0) return s;
+  if (T < 0 || T > a.max_new || c0 < 0 || c1 > a.total || len < 0 ||
+      ((L - 1) >> a.c.page_shift) >= a.c.max_pages) {
+    if (flag) flag_range(a.c);
+    return s;
+  }
+  s.T = (int)T;
+  s.len = len;
+  s.cu0 = c0;
+  s.RT = (int)(((long long)s.T * a.G + a.tile_rows - 1) / a.tile_rows);
+  s.KT = (int)((L + kChunk - 1) / kChunk);
+  return s;
+}
+
+// A place in the line of chunks: sequence b, unit u = key head * RT + row tile, chunk kt.
+struct Cursor {
+  SeqView s;
+  int b, u, kt;
+  int h;                         // the unit's key head
+  int last;                      // last key position that a row of the unit may see
+};
+
+__device__ __forceinline__ void enter_unit(const TreeArgs& a, Cursor& c) {
+  c.h = c.u / c.s.RT;
+  c.last = c.s.len + c.s.T - 1;
+  if (a.mask == nullptr) {       // chain: up to the row tile's last token
+    const long long end = ((long long)(c.u - c.h * c.s.RT + 1) * a.tile_rows + a.G - 1) / a.G;
+    if (end < c.s.T) c.last = c.s.len + (int)end - 1;
+  }
+}
+
+// CTA cta's part of the line: n chunks from lo.  No part is empty while another has two.
+struct Part {
+  long long lo;
+  int n;
+};
+__device__ __forceinline__ Part part_of(long long total, int cta, int ctas) {
+  const long long C = min((long long)ctas, total);
+  if (cta >= C) return Part{0, 0};
+  const long long lo = total * cta / C, hi = total * (cta + 1) / C;
+  return Part{lo, (int)(hi - lo)};
+}
+// The CTA whose part holds chunk g.
+__device__ __forceinline__ int owner_cta(long long total, long long g, int ctas) {
+  const long long C = min((long long)ctas, total);
+  return (int)(((g + 1) * C - 1) / total);
+}
+
+// Total chunks (every lane of a warp gets it).
+__device__ __forceinline__ long long total_chunks(const TreeArgs& a, bool flag) {
+  const int lane = threadIdx.x & 31;
+  long long n = 0;
+  for (int b = lane; b < a.c.B; b += 32) {
+    const SeqView s = load_seq(a, b, flag);
+    n += (long long)s.RT * s.KT * a.c.Hk;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n;
+}
+
+// The place of chunk g (below the total); one warp together.
+__device__ __forceinline__ Cursor locate(const TreeArgs& a, long long g) {
+  const int lane = threadIdx.x & 31;
+  Cursor c{};
+  for (int base = 0; base < a.c.B; base += 32) {
+    SeqView s{0, 0, 0, 0, 0};
+    if (base + lane < a.c.B) s = load_seq(a, base + lane, false);
+    const long long n = (long long)s.RT * s.KT * a.c.Hk;
+    long long inc = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += t;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, inc > g);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      const long long before = __shfl_sync(0xffffffffu, inc - n, src);
+      c.b = base + src;
+      c.s.T = __shfl_sync(0xffffffffu, s.T, src);
+      c.s.len = __shfl_sync(0xffffffffu, s.len, src);
+      c.s.cu0 = __shfl_sync(0xffffffffu, s.cu0, src);
+      c.s.RT = __shfl_sync(0xffffffffu, s.RT, src);
+      c.s.KT = __shfl_sync(0xffffffffu, s.KT, src);
+      const long long r = g - before;
+      c.u = (int)(r / c.s.KT);
+      c.kt = (int)(r - (long long)c.u * c.s.KT);
+      enter_unit(a, c);
+      return c;
+    }
+    g -= __shfl_sync(0xffffffffu, inc, 31);
+  }
+  return c;
+}
+
+// The next chunk; only called while chunks are left.
+__device__ __forceinline__ void next_unit(const TreeArgs& a, Cursor& c) {
+  c.kt = 0;
+  if (++c.u >= c.s.RT * a.c.Hk) {
+    c.u = 0;
+    do {
+      if (++c.b >= a.c.B) return;
+      c.s = load_seq(a, c.b, false);
+    } while (c.s.T == 0);
+  }
+  enter_unit(a, c);
+}
+
+// Host side (fa_cache.cu): checks of the cache argument, and its view.
+int check_cache(const fa_cache& c);
+CacheView view_of(const fa_cache& c);
+// fa_host.cu: what fa_last_launch_count returns, and the TMA map of a cache's rows [rows][d] in
+// boxes of box_rows whole rows, 128-byte panels (64-byte rows for E4M3 at d = 64), swizzled.
+void note_launches(int n);
+bool encode_cache(CUtensorMap* m, const void* base, long long rows, int d, int elem, int box_rows);
+
+}  // namespace fa

@@ -1,0 +1,818 @@
+// fa_tree.cu -- attention of the new tokens of each sequence (one token, a chain, or a tree of
+// drafted tokens) over the paged key/value cache, and the merge of units cut between CTAs.
+//
+// Row (t, g) of key head h is query head h * G + g of new token t.  It sees key position p when p <
+// len (the prefix) or when new token p - len is visible to t (mask bit, or p - len <= t):
+//     O = sum_p 2^(s_p - m) v_p / sum_p 2^(s_p - m),  s_p = scale * log2(e) * q . k_p,
+// in one pass over the keys with a running max m and sum l (online softmax).
+//
+// This file's kernel is the one for few rows per key head (decoding, small trees), where the cache is
+// read once and its bytes are the bound.  One CTA per SM, eight warps.  A chunk of 128 keys is
+// eight steps of 16 keys; warp w always takes step w, with a ring of its own that its lane 0 fills by
+// TMA several steps ahead, so warps never wait for one another inside a segment and loads cross
+// from one unit to the next without a pause.  Each warp keeps its own m, l and O (16 * kMT rows,
+// mma.sync m16n8k16 fragments in registers); at the end of a segment (the CTA's run of chunks of one
+// unit) the eight are merged through shared memory.
+#include <climits>
+#include <cmath>
+
+#include "fa.h"
+#include "fa_cache.cuh"
+#include "sm100.cuh"
+
+namespace fa {
+
+namespace {
+
+constexpr float kLn2f = 0.693147180559945309f;
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool kFp16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kFp16)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Two E4M3 codes in bytes 1 and 3 of x (the others zero) to two bf16: sign to bit 15, the seven
+// exponent and mantissa bits to bits 10..4, which reads as value * 2^-120 (bias 7 under bias 127;
+// E4M3's subnormals become bf16's); the product with 2^120 is exact.  The NaN code (all seven
+// bits set) would read as 480, so it is handled apart (see any_nan_code).
+__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x) {
+  const uint32_t r = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
+  __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&r);
+  const uint32_t k = 0x7B807B80u;                   // 2^120
+  v = __hmul2(v, *reinterpret_cast<const __nv_bfloat162*>(&k));
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+// Bytes (i, j) of w as two 16-bit floats.
+template <bool kFp16, int i, int j>
+__device__ __forceinline__ uint32_t expand2(uint32_t w) {
+  if constexpr (kFp16) return e4m3_to_f16x2(__byte_perm(w, 0, i | (j << 4)));
+  else return codes_to_bf16x2(__byte_perm(w, 0, 4 | (i << 4) | (4 << 8) | (j << 12)));
+}
+// Whether one of the four codes is NaN (0x7F or 0xFF).
+__device__ __forceinline__ bool any_nan_code(uint32_t w) {
+  return ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u);
+}
+
+template <int D, bool kFp8>
+struct SmallCfg {
+  static constexpr int kEsz = kFp8 ? 1 : 2;
+  static constexpr int kHalf = 16 * D * kEsz;            // 16 rows of K (or V)
+  static constexpr int kStage = 2 * kHalf;
+  static constexpr int kStages = kFp8 ? 20480 / kStage : 24576 / kStage;
+  static constexpr int kRing = 8 * kStages * kStage;     // all warps
+  static constexpr int kSlot = 16 * D * 4 + 128;         // one warp's O, m and l of 16 rows
+  static constexpr int kScales = kFp8 ? 8 * kStages * 32 : 0;
+  static constexpr int kSmem = kRing + 4 * kSlot + kScales + 1024;
+  // bytes between 16-byte chunks' rows: 128-byte panels (64-byte rows for E4M3 at d = 64)
+  static constexpr int kRowB = D * kEsz < 128 ? 64 : 128;
+};
+
+// Shared-memory offset of 16-byte chunk c of row r in a 16-row K or V stage as TMA wrote it.
+template <int D, bool kFp8>
+__device__ __forceinline__ uint32_t swz(int r, int c) {
+  if constexpr (SmallCfg<D, kFp8>::kRowB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  else return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+template <int D, bool kFp8, bool kFp16, int kMT>
+__global__ void __launch_bounds__(256, 1)
+    tree_small_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                      const TreeArgs a) {
+  using C = SmallCfg<D, kFp8>;
+  constexpr int kNT = D / 8;                              // 8-column tiles of O
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  __shared__ uint64_t full[8][C::kStages];
+  __shared__ int abort_flag;
+  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
+  uint8_t* base = smem_raw + pad;
+  const int warp = warp_id(), lane = lane_id();
+  uint8_t* ring = base + warp * C::kStages * C::kStage;
+  uint8_t* slots = base + C::kRing;
+  uint8_t* scales = slots + 4 * C::kSlot + warp * C::kStages * 32;
+  const DevStatus st{a.c.status, a.timeout_ns};
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (lane == 0)
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[warp][i], 1);
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    prefetch_tmap(&tm_k);
+    prefetch_tmap(&tm_v);
+  }
+  fence_barrier_init();
+  __syncthreads();
+
+  const long long total = total_chunks(a, blockIdx.x == 0 && warp == 0);
+  const Part part = part_of(total, blockIdx.x, gridDim.x);
+  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (part.n == 0) return;
+  Cursor rd = locate(a, part.lo), ld = rd;
+  int rd_left = part.n, ld_left = part.n;
+
+  // ---------------------------------------------------------------- loads
+  // A step is loaded when its first key exists and some row of the tile may see it.
+  auto wanted = [&](const Cursor& c) { return c.kt * kChunk + warp * 16 <= c.last; };
+  int issued = 0, used = 0;                               // stages filled and consumed
+  bool ok = true;
+  auto advance = [&](Cursor& c, int& left) {
+    --left;
+    if (++c.kt < c.s.KT) return;
+    if (left > 0) next_unit(a, c);
+  };
+  auto fill = [&]() {                                     // start the next wanted step's copy, if any
+    while (ld_left > 0) {
+      const bool w = wanted(ld);
+      if (w) {
+        if (lane == 0) {
+          const int p0 = ld.kt * kChunk + warp * 16;
+          long long row = slot_row(a.c, ld.b, ld.h, p0);
+          if (row < 0) row = 0;                           // flagged; stay inside the cache
+          const int stg = issued % C::kStages;
+          uint64_t* bar = &full[warp][stg];
+          mbar_arrive_expect_tx(bar, C::kStage + (kFp8 ? 32 : 0));
+          tma_load_3d(ring + stg * C::kStage, &tm_k, bar, 0, (int)row, 0);
+          tma_load_3d(ring + stg * C::kStage + C::kHalf, &tm_v, bar, 0, (int)row, 0);
+          if constexpr (kFp8) {
+            bulk_load(scales + stg * 32, a.c.ks + row, 16, bar);
+            bulk_load(scales + stg * 32 + 16, a.c.vs + row, 16, bar);
+          }
+        }
+        ++issued;
+      }
+      advance(ld, ld_left);
+      if (w) return;
+    }
+  };
+  for (int i = 0; i < C::kStages; ++i) fill();
+
+  // ---------------------------------------------------------------- segments
+  const int r0 = lane >> 2, tq = lane & 3;                // fragment row and column quad
+  while (rd_left > 0) {
+    const SeqView s = rd.s;
+    const int h = rd.h;
+    const int row0 = (rd.u - h * s.RT) * a.tile_rows;
+    const int nrows = (int)min((long long)a.tile_rows, (long long)s.T * a.G - row0);
+    const bool from_start = rd.kt == 0;
+    const int seg_unit = rd.u, seg_b = rd.b;
+    const long long seg_g = part.lo + (part.n - rd_left);  // the segment's first chunk in the line
+
+    // Q fragments; rows past the unit's last read the last one (never stored)
+    uint32_t qf[kMT][D / 16][4];
+    int tok[kMT][2];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        const int r = row0 + min(mt * 16 + hf * 8 + r0, nrows - 1);
+        const int t = r / a.G, g = r - t * a.G;
+        tok[mt][hf] = t;
+        const uint16_t* qp = a.q + (s.cu0 + t) * a.q_tok + (h * a.G + g) * a.q_head;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          if constexpr (kFp8) {
+            // the order of the 16 columns of a step is free as long as K's agrees: a lane's
+            // four E4M3 columns 4 tq .. 4 tq + 3 stand at places (2tq, 2tq+1, 2tq+8, 2tq+9)
+            const uint2 w = *reinterpret_cast<const uint2*>(qp + kk * 16 + 4 * tq);
+            qf[mt][kk][hf] = w.x;
+            qf[mt][kk][hf + 2] = w.y;
+          } else {
+            qf[mt][kk][hf] = *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 2 * tq);
+            qf[mt][kk][hf + 2] = *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 8 + 2 * tq);
+          }
+        }
+      }
+    float o[kMT][kNT][4], m[kMT][2], l[kMT][2];
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
+      m[mt][0] = m[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+    }
+
+    // ------------------------------------------------------------ the segment's steps
+    bool more = true;
+    while (more) {
+      if (wanted(rd)) {
+        const int stg = used % C::kStages;
+        if (ok) ok = mbar_wait(&full[warp][stg], (used / C::kStages) & 1, &abort_flag, st);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) {
+          const uint8_t* sk = ring + stg * C::kStage;
+          const uint32_t ak = smem_addr(sk), av = ak + C::kHalf;
+          const int p0 = rd.kt * kChunk + warp * 16;
+          // ---- S = Q K^T, 16 * kMT rows x 16 keys
+          float sc[kMT][2][4];
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) sc[mt][j][i] = 0.f;
+          float kf[2][2] = {{1.f, 1.f}, {1.f, 1.f}}, vf[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
+          uint32_t vh[2] = {0, 0};                        // fp16: scales of V's key pairs
+          bool odd = false;                               // a value in this lane's V codes is not finite
+          if constexpr (kFp8) {
+            const uint8_t* sp = scales + stg * 32;
+            uint32_t nan_k = 0;                           // keys (rows of K) with a NaN code
+#pragma unroll
+            for (int c = 0; c < D / 16; c += 2) {
+              uint32_t kr[4];
+              ldsm4(ak + swz<D, true>((lane & 7) + ((lane >> 3) & 1) * 8, c + (lane >> 4)), kr);
+              if constexpr (!kFp16)
+                nan_k |= (any_nan_code(kr[0]) || any_nan_code(kr[2]) ? 1u : 0u) |
+                         (any_nan_code(kr[1]) || any_nan_code(kr[3]) ? 2u : 0u);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t a0 = expand2<kFp16, 0, 1>(kr[j]), a1 = expand2<kFp16, 2, 3>(kr[j]);
+                const uint32_t b0 = expand2<kFp16, 0, 1>(kr[2 + j]), b1 = expand2<kFp16, 2, 3>(kr[2 + j]);
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) {
+                  mma16816<kFp16>(sc[mt][j], qf[mt][c], a0, a1);
+                  mma16816<kFp16>(sc[mt][j], qf[mt][c + 1], b0, b1);
+                }
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const uint32_t wk = *reinterpret_cast<const uint16_t*>(sp + 8 * j + 2 * tq);
+              const uint32_t wv = *reinterpret_cast<const uint16_t*>(sp + 16 + 8 * j + 2 * tq);
+              kf[j][0] = scale_value(wk & 0xFF);
+              kf[j][1] = scale_value(wk >> 8);
+              // bf16: P carries 2^e.  fp16: V does, down to 2^-24 (the type's last bit); P the rest
+              const int e0 = (int)(wv & 0xFF) - 127, e1 = (int)(wv >> 8) - 127;
+              if constexpr (kFp16) {
+                vh[j] = pack2<true>(scale_value(max(e0, -24) + 127), scale_value(max(e1, -24) + 127));
+                vf[j][0] = scale_value(min(e0 + 24, 0) + 127);
+                vf[j][1] = scale_value(min(e1 + 24, 0) + 127);
+              } else {
+                vf[j][0] = scale_value(wv & 0xFF);
+                vf[j][1] = scale_value(wv >> 8);
+              }
+            }
+            if constexpr (!kFp16) {
+              if (__any_sync(0xffffffffu, nan_k != 0)) {  // rare: a key that holds NaN scores NaN
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                  const unsigned bal = __ballot_sync(0xffffffffu, (nan_k >> j) & 1);
+#pragma unroll
+                  for (int i = 0; i < 2; ++i)
+                    if ((bal >> (4 * (2 * tq + i))) & 0xFu) kf[j][i] = __int_as_float(0x7FFFFFFF);
+                }
+              }
+            }
+          } else {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              uint32_t kr[4];
+              ldsm4(ak + swz<D, false>((lane & 7) + (lane >> 4) * 8, 2 * kk + ((lane >> 3) & 1)), kr);
+#pragma unroll
+              for (int mt = 0; mt < kMT; ++mt) {
+                mma16816<kFp16>(sc[mt][0], qf[mt][kk], kr[0], kr[1]);
+                mma16816<kFp16>(sc[mt][1], qf[mt][kk], kr[2], kr[3]);
+              }
+            }
+          }
+          // ---- scale, mask, online softmax
+          const bool masked = p0 + 16 > s.len;
+          uint32_t pf[kMT][4];
+          unsigned see[kMT][2];                           // bit 2j + i: key 8j + 2 tq + i is visible
+#pragma unroll
+          for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+              float x[2][2];
+              see[mt][hf] = 0xF;
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) x[j][i] = sc[mt][j][2 * hf + i] * (kFp8 ? a.scale_log2 * kf[j][i] : a.scale_log2);
+              if (masked) {
+                const int t = tok[mt][hf];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) {
+                    const int n = p0 + 8 * j + 2 * tq + i - s.len;     // new token of this key
+                    bool vis = n < 0;
+                    if (n >= 0 && n < s.T) {
+                      if (a.mask == nullptr) vis = n <= t;
+                      else vis = (n >> 6) < a.words &&
+                                 ((a.mask[(long long)(s.cu0 + t) * a.words + (n >> 6)] >> (n & 63)) & 1);
+                    }
+                    if (!vis) {
+                      x[j][i] = -INFINITY;
+                      see[mt][hf] &= ~(1u << (2 * j + i));
+                    }
+                  }
+              }
+              float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+              const float mn = fmaxf(m[mt][hf], mx);
+              const float neg = mn == -INFINITY ? 0.f : -mn;
+              const float al = ex2(m[mt][hf] + neg);      // 0 while m = -inf
+              m[mt][hf] = mn;
+              float sum = 0.f;
+              float p[2][2];
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  p[j][i] = ex2(x[j][i] + neg);
+                  sum += p[j][i];
+                }
+              l[mt][hf] = l[mt][hf] * al + sum;
+              if (__any_sync(0xffffffffu, al != 1.f)) {
+#pragma unroll
+                for (int n = 0; n < kNT; ++n) {
+                  o[mt][n][2 * hf] *= al;
+                  o[mt][n][2 * hf + 1] *= al;
+                }
+              }
+              // P to 16 bits, one rounding of at most half a step (the row sum keeps 32 bits); a
+              // masked key's scale may be anything, so its zero is not multiplied
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                if constexpr (kFp8) {
+#pragma unroll
+                  for (int i = 0; i < 2; ++i) p[j][i] = masked && !((see[mt][hf] >> (2 * j + i)) & 1) ? 0.f : p[j][i] * vf[j][i];
+                }
+                pf[mt][hf + 2 * j] = pack2<kFp16>(p[j][0], p[j][1]);
+              }
+            }
+          }
+          // ---- O += P V
+          // Past the sequence's last key the page holds anything: those rows of V count as zero.
+          uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
+          if (masked) {
+            const int end = s.len + s.T - p0 - 2 * tq;     // keys from here on do not exist
+            keep0 = (end > 0 ? 0xFFFFu : 0u) | (end > 1 ? 0xFFFF0000u : 0u);
+            keep1 = (end > 8 ? 0xFFFFu : 0u) | (end > 9 ? 0xFFFF0000u : 0u);
+          }
+          auto vfrag = [&](int c, uint32_t (&b)[4]) {      // V of columns 16 c .. 16 c + 15: two tiles
+            uint32_t vr[4];
+            if constexpr (kFp8) {
+              // one chunk of 16 columns; lanes 16..31 fetch the same rows of the next chunk
+              ldsm4t(av + swz<D, true>((lane & 7) + ((lane >> 3) & 1) * 8, (c & ~1) + (lane >> 4)), vr);
+              const uint32_t lo8 = (c & 1) ? vr[2] : vr[0], hi8 = (c & 1) ? vr[3] : vr[1];
+              if constexpr (!kFp16) {
+                if (any_nan_code(lo8) || any_nan_code(hi8)) odd = true;
+              }
+              b[0] = expand2<kFp16, 0, 2>(lo8);
+              b[1] = expand2<kFp16, 0, 2>(hi8);
+              b[2] = expand2<kFp16, 1, 3>(lo8);
+              b[3] = expand2<kFp16, 1, 3>(hi8);
+              if constexpr (kFp16) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  __half2 x = *reinterpret_cast<__half2*>(&b[i]);
+                  x = __hmul2(x, *reinterpret_cast<const __half2*>(&vh[i & 1]));
+                  b[i] = *reinterpret_cast<uint32_t*>(&x);
+                }
+              }
+            } else {
+              ldsm4t(av + swz<D, false>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * c + (lane >> 4)), vr);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) b[i] = vr[i];
+            }
+          };
+          // The products one by one, visible keys only.  poison: only what NaN codes add.
+          auto one_by_one = [&](bool poison) {
+            const int live = min(16, s.len + s.T - p0);
+            for (int key = 0; key < live; ++key) {
+              const int src = (lane & ~3) | ((key & 7) >> 1), j = key >> 3, i = key & 1;
+              float w[kMT][2];
+              bool v[kMT][2];
+#pragma unroll
+              for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                  const float2 f = unpack2<kFp16>(__shfl_sync(0xffffffffu, j ? pf[mt][hf + 2] : pf[mt][hf], src));
+                  w[mt][hf] = i ? f.y : f.x;
+                  v[mt][hf] = (__shfl_sync(0xffffffffu, see[mt][hf], src) >> (2 * j + i)) & 1;
+                }
+              float sv = 1.f;
+              if constexpr (kFp8 && kFp16) sv = scale_value(max((int)scales[stg * 32 + 16 + key], 127 - 24));
+#pragma unroll
+              for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                  float x;                                // V[key][column of accumulator (n, e)]
+                  if constexpr (kFp8) {
+                    const int col = 16 * (n >> 1) + 4 * tq + 2 * e + (n & 1);
+                    const uint32_t code = sk[C::kHalf + swz<D, true>(key, col >> 4) + (col & 15)];
+                    const bool nan = (code & 0x7F) == 0x7F;
+                    x = poison && !nan ? 0.f : nan ? __int_as_float(0x7FFFFFFF) : unpack2<true>(e4m3_to_f16x2(code)).x * sv;
+                  } else {
+                    const int col = 8 * n + 2 * tq + e;
+                    x = unpack2<kFp16>(*reinterpret_cast<const uint16_t*>(sk + C::kHalf + swz<D, false>(key, col >> 3) +
+                                                                          2 * (col & 7))).x;
+                  }
+#pragma unroll
+                  for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                    for (int hf = 0; hf < 2; ++hf)
+                      if (v[mt][hf]) o[mt][n][2 * hf + e] += w[mt][hf] * x;
+                }
+            }
+          };
+          // A masked product is 0 * v, which is not 0 where v is not finite: a step of new tokens
+          // whose values are not all finite is done one by one.
+          bool apart = false;
+          if (masked) {
+            bool bad = false;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t b[4];
+              vfrag(c, b);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t w = b[i] & ((i & 1) ? keep1 : keep0);
+                const uint32_t e = kFp16 ? 0x7C00u : 0x7F80u;
+                bad |= (w & e) == e || ((w >> 16) & e) == e;
+              }
+            }
+            apart = __any_sync(0xffffffffu, bad || odd);
+            odd = false;
+          }
+          if (apart) {
+            one_by_one(false);
+          } else {
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            uint32_t b[4];
+            vfrag(c, b);
+            if (masked) {
+              b[0] &= keep0;
+              b[1] &= keep1;
+              b[2] &= keep0;
+              b[3] &= keep1;
+            }
+#pragma unroll
+            for (int mt = 0; mt < kMT; ++mt) {
+              mma16816<kFp16>(o[mt][2 * c], pf[mt], b[0], b[1]);
+              mma16816<kFp16>(o[mt][2 * c + 1], pf[mt], b[2], b[3]);
+            }
+          }
+          if constexpr (kFp8 && !kFp16) {                 // NaN codes went in as numbers
+            if (__any_sync(0xffffffffu, odd)) one_by_one(true);
+          }
+          }
+        }
+        ++used;
+        __syncwarp();                                     // the stage has been read: refill it
+        if (ok) fill();
+      }
+      const int kt = rd.kt + 1;
+      more = kt < s.KT && rd_left > 1;
+      advance(rd, rd_left);
+    }
+    const bool to_end = rd_left > 0 || rd.kt >= s.KT;
+
+    // ------------------------------------------------------------ merge of the eight warps
+#pragma unroll
+    for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+      for (int hf = 0; hf < 2; ++hf) {
+        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
+        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
+      }
+      for (int half = 4; half > 0; half >>= 1) {
+        __syncthreads();
+        if (warp >= half && warp < 2 * half) {
+          uint8_t* sl = slots + (warp - half) * C::kSlot;
+          float4* so = reinterpret_cast<float4*>(sl);
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) so[n * 32 + lane] = make_float4(o[mt][n][0], o[mt][n][1], o[mt][n][2], o[mt][n][3]);
+          float* sm = reinterpret_cast<float*>(sl + 16 * D * 4);
+          if (tq == 0) {
+            sm[r0] = m[mt][0];
+            sm[r0 + 8] = m[mt][1];
+            sm[16 + r0] = l[mt][0];
+            sm[24 + r0] = l[mt][1];
+          }
+        }
+        __syncthreads();
+        if (warp < half) {
+          const uint8_t* sl = slots + warp * C::kSlot;
+          const float4* so = reinterpret_cast<const float4*>(sl);
+          const float* sm = reinterpret_cast<const float*>(sl + 16 * D * 4);
+          float fa[2], fb[2];
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            const float mb = sm[r0 + 8 * hf], lb = sm[16 + r0 + 8 * hf];
+            const float mn = fmaxf(m[mt][hf], mb);
+            const float neg = mn == -INFINITY ? 0.f : -mn;
+            fa[hf] = ex2(m[mt][hf] + neg);
+            fb[hf] = ex2(mb + neg);
+            m[mt][hf] = mn;
+            l[mt][hf] = l[mt][hf] * fa[hf] + lb * fb[hf];
+          }
+#pragma unroll
+          for (int n = 0; n < kNT; ++n) {
+            const float4 w = so[n * 32 + lane];
+            o[mt][n][0] = o[mt][n][0] * fa[0] + w.x * fb[0];
+            o[mt][n][1] = o[mt][n][1] * fa[0] + w.y * fb[0];
+            o[mt][n][2] = o[mt][n][2] * fa[1] + w.z * fb[1];
+            o[mt][n][3] = o[mt][n][3] * fa[1] + w.w * fb[1];
+          }
+        }
+      }
+    }
+
+    // ------------------------------------------------------------ results
+    // A whole unit is normalised and stored; a cut one leaves its sums to the merge: slot 0 of this
+    // CTA for a segment that began in an earlier CTA, slot 1 for one that only begins here.
+    if (warp == 0) {
+      const bool whole = from_start && to_end;
+      const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
+      if (lane == 0 && from_start && !to_end) a.meta[blockIdx.x] = make_int4(seg_b, seg_unit, owner_cta(total, seg_g + s.KT - 1, gridDim.x), 0);
+#pragma unroll
+      for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          const int r = mt * 16 + hf * 8 + r0;
+          if (r >= nrows) continue;
+          const float lv = l[mt][hf];
+          if (whole) {
+            const float inv = lv == 0.f ? 0.f : 1.f / lv;
+            const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
+            const long long tk = s.cu0 + t;
+            const int hq = h * a.G + g;
+            if (tq == 0) a.lse[tk * a.Hq + hq] = lv == 0.f ? -INFINITY : (m[mt][hf] + log2f(lv)) * kLn2f;
+            uint16_t* op = a.o + tk * a.o_tok + hq * a.o_head;
+            if constexpr (kFp8) {
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c)
+                *reinterpret_cast<uint2*>(op + 16 * c + 4 * tq) =
+                    make_uint2(pack2<kFp16>(o[mt][2 * c][2 * hf] * inv, o[mt][2 * c + 1][2 * hf] * inv),
+                               pack2<kFp16>(o[mt][2 * c][2 * hf + 1] * inv, o[mt][2 * c + 1][2 * hf + 1] * inv));
+            } else {
+#pragma unroll
+              for (int n = 0; n < kNT; ++n)
+                *reinterpret_cast<uint32_t*>(op + 8 * n + 2 * tq) =
+                    pack2<kFp16>(o[mt][n][2 * hf] * inv, o[mt][n][2 * hf + 1] * inv);
+            }
+          } else {
+            float* pp = a.part_o + ((long long)slot * a.tile_rows + r) * D;
+            if (tq == 0) {
+              float* ml = a.part_ml + ((long long)slot * a.tile_rows + r) * 2;
+              ml[0] = m[mt][hf];
+              ml[1] = lv;
+            }
+            if constexpr (kFp8) {
+#pragma unroll
+              for (int c = 0; c < D / 16; ++c)
+                *reinterpret_cast<float4*>(pp + 16 * c + 4 * tq) =
+                    make_float4(o[mt][2 * c][2 * hf], o[mt][2 * c + 1][2 * hf], o[mt][2 * c][2 * hf + 1],
+                                o[mt][2 * c + 1][2 * hf + 1]);
+            } else {
+#pragma unroll
+              for (int n = 0; n < kNT; ++n)
+                *reinterpret_cast<float2*>(pp + 8 * n + 2 * tq) =
+                    make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
+            }
+          }
+        }
+    }
+  }
+  // A wait that ran out left copies in flight: let them land before the shared memory goes away.
+  if (!ok && lane == 0)
+    for (int i = max(used, issued - C::kStages); i < issued; ++i)
+      mbar_wait_drain(&full[warp][i % C::kStages], (i / C::kStages) & 1, st);
+}
+
+// ------------------------------------------------------------------------------------
+// Merge of the units cut between CTAs: block (c, y) takes the unit that begins in CTA c and ends in
+// a later one, a warp one of its rows.  With parts (m_i, l_i, O_i):
+//     O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i.
+// ------------------------------------------------------------------------------------
+template <int D, bool kFp16>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
+  constexpr int kV = D / 32;                              // columns per lane
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, lane = lane_id();
+  const int4 me = a.meta[c];
+  if (me.x < 0) return;
+  const SeqView s = load_seq(a, me.x, false);
+  const int h = me.y / s.RT, rt = me.y - h * s.RT;
+  const int row0 = rt * a.tile_rows;
+  const int nrows = (int)min((long long)a.tile_rows, (long long)s.T * a.G - row0);
+  const int r = blockIdx.y * 8 + warp_id();
+  if (r >= nrows) return;
+  const int n = me.z - c + 1;                             // parts: this CTA's and those of c + 1 .. me.z
+  float m = -INFINITY;
+  for (int i = lane; i < n; i += 32) {
+    const long long slot = i == 0 ? 2LL * c + 1 : 2LL * (c + i);
+    m = fmaxf(m, a.part_ml[(slot * a.tile_rows + r) * 2]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float neg = m == -INFINITY ? 0.f : -m;
+  float l = 0.f, acc[kV] = {};
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    float w = 0.f;
+    if (i0 + lane < n) {
+      const long long slot = i0 + lane == 0 ? 2LL * c + 1 : 2LL * (c + i0 + lane);
+      const float* ml = a.part_ml + (slot * a.tile_rows + r) * 2;
+      w = ex2(ml[0] + neg);
+      l += w * ml[1];
+    }
+    const int k = min(32, n - i0);
+#pragma unroll 8
+    for (int i = 0; i < k; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      const long long slot = i0 + i == 0 ? 2LL * c + 1 : 2LL * (c + i0 + i);
+      const float* p = a.part_o + (slot * a.tile_rows + r) * D + lane * kV;
+      if constexpr (kV == 4) {
+        const float4 x = *reinterpret_cast<const float4*>(p);
+        acc[0] += wi * x.x;
+        acc[1] += wi * x.y;
+        acc[2] += wi * x.z;
+        acc[3] += wi * x.w;
+      } else {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        acc[0] += wi * x.x;
+        acc[1] += wi * x.y;
+      }
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
+  const long long tk = s.cu0 + t;
+  const int hq = h * a.G + g;
+  if (lane == 0) a.lse[tk * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2f;
+  uint32_t* op = reinterpret_cast<uint32_t*>(a.o + tk * a.o_tok + hq * a.o_head + lane * kV);
+#pragma unroll
+  for (int i = 0; i < kV; i += 2) op[i / 2] = pack2<kFp16>(acc[i] * inv, acc[i + 1] * inv);
+}
+
+template <int D, bool kFp8, bool kFp16, int kMT>
+cudaError_t launch_small(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, cudaStream_t s) {
+  auto kern = tree_small_kernel<D, kFp8, kFp16, kMT>;
+  constexpr int smem = SmallCfg<D, kFp8>::kSmem;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kern<<<ctas, 256, smem, s>>>(tk, tv, a);
+  return cudaGetLastError();
+}
+
+template <int D, bool kFp8, bool kFp16>
+cudaError_t launch_small_mt(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, cudaStream_t s) {
+  return a.tile_rows == 16 ? launch_small<D, kFp8, kFp16, 1>(tk, tv, a, ctas, s)
+                           : launch_small<D, kFp8, kFp16, 2>(tk, tv, a, ctas, s);
+}
+
+template <int D>
+cudaError_t launch_small_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp8, bool fp16,
+                           int ctas, cudaStream_t s) {
+  if (fp8) return fp16 ? launch_small_mt<D, true, true>(tk, tv, a, ctas, s) : launch_small_mt<D, true, false>(tk, tv, a, ctas, s);
+  return fp16 ? launch_small_mt<D, false, true>(tk, tv, a, ctas, s) : launch_small_mt<D, false, false>(tk, tv, a, ctas, s);
+}
+
+// Launched so that its blocks may start while the attention kernel still runs (they wait for its
+// end on the device): saves most of a launch's latency.
+template <int D, bool kFp16>
+cudaError_t launch_merge_d(const TreeArgs& a, int ctas, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(ctas, (a.tile_rows + 7) / 8, 1);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kFp16>, a);
+}
+
+struct TreeLayout {
+  size_t part_ml, meta, total;
+};
+
+// Partial sums of at most two cut units per CTA.
+TreeLayout tree_layout(int rows, int d) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  TreeLayout w;
+  w.part_ml = up((size_t)kTreeCtas * 2 * rows * d * 4);
+  w.meta = w.part_ml + up((size_t)kTreeCtas * 2 * rows * 8);
+  w.total = w.meta + up((size_t)kTreeCtas * sizeof(int4));
+  return w;
+}
+
+// Most rows a row tile can have in a call with this many new tokens.
+int most_rows(int total, int G) {
+  const long long r = ((long long)total * G + 15) / 16 * 16;
+  return (int)(r < 32 ? r : 32);
+}
+
+bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+}  // namespace
+}  // namespace fa
+
+using namespace fa;
+
+extern "C" {
+
+size_t fa_fwd_tree_workspace_bytes(int total, int Hq, int Hk, int d) {
+  if (total < 0 || Hk < 1 || Hq < Hk || Hq % Hk != 0 || (d != 64 && d != 128)) return 0;
+  return tree_layout(most_rows(total > 0 ? total : 1, Hq / Hk), d).total;
+}
+
+int fa_fwd_tree(const fa_fwd_tree_args* p) {
+  if (p == nullptr) return FA_ERR_INVALID_ARG;
+  const fa_fwd_tree_args& x = *p;
+  int rc = check_cache(x.cache);
+  if (rc != FA_OK) return rc;
+  if (x.dtype != FA_BF16 && x.dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
+  if (x.cache.dtype != FA_E4M3 && x.cache.dtype != x.dtype) return FA_ERR_UNSUPPORTED;
+  if (!(x.scale > 0.f) || !std::isfinite(x.scale)) return FA_ERR_INVALID_ARG;
+  if (x.total < 0 || x.max_new < 0 || x.Hq < 1 || x.Hq % x.cache.Hk != 0) return FA_ERR_INVALID_ARG;
+  if (!x.cu_new || !x.lens || !aligned(x.cu_new, 4) || !aligned(x.lens, 4)) return FA_ERR_INVALID_ARG;
+  if (x.tree_mask != nullptr && (x.mask_words < 1 || (long long)x.mask_words * 64 < x.max_new)) return FA_ERR_INVALID_ARG;
+  if (!aligned(x.tree_mask, 8)) return FA_ERR_INVALID_ARG;
+  if (x.total == 0 || x.max_new == 0) return FA_OK;
+  if (!x.q || !x.o || !x.lse || !aligned(x.q, 16) || !aligned(x.o, 16) || !aligned(x.lse, 4)) return FA_ERR_INVALID_ARG;
+  for (const long long s : {(long long)x.q_token_stride, (long long)x.q_head_stride, (long long)x.o_token_stride,
+                            (long long)x.o_head_stride})
+    if (s < 0 || s % 8 != 0) return FA_ERR_INVALID_ARG;
+  const int G = x.Hq / x.cache.Hk;
+  if ((long long)x.max_new * G > INT_MAX - 256) return FA_ERR_UNSUPPORTED;
+  const TreeLayout w = tree_layout(most_rows(x.total, G), x.cache.d);
+  if (!x.workspace || !aligned(x.workspace, 256) || x.workspace_bytes < w.total) return FA_ERR_WORKSPACE;
+
+  const bool fp8 = x.cache.dtype == FA_E4M3, fp16 = x.dtype == FA_FP16;
+  TreeArgs a{};
+  a.c = view_of(x.cache);
+  if (!a.c.status) return FA_ERR_CUDA;
+  a.q = static_cast<const uint16_t*>(x.q);
+  a.o = static_cast<uint16_t*>(x.o);
+  a.lse = x.lse;
+  a.cu = x.cu_new;
+  a.lens = x.lens;
+  a.mask = reinterpret_cast<const unsigned long long*>(x.tree_mask);
+  a.words = x.mask_words;
+  uint8_t* ws = static_cast<uint8_t*>(x.workspace);
+  a.part_o = reinterpret_cast<float*>(ws);
+  a.part_ml = reinterpret_cast<float*>(ws + w.part_ml);
+  a.meta = reinterpret_cast<int4*>(ws + w.meta);
+  a.q_tok = x.q_token_stride; a.q_head = x.q_head_stride;
+  a.o_tok = x.o_token_stride; a.o_head = x.o_head_stride;
+  a.total = x.total;
+  a.Hq = x.Hq;
+  a.G = G;
+  a.max_new = x.max_new;
+  a.timeout_ns = 2000000000ull;
+  a.scale_log2 = (float)((double)x.scale * 1.4426950408889634);
+  a.tile_rows = (long long)min(x.max_new, x.total) * G <= 16 ? 16 : 32;
+
+  CUtensorMap tk, tv;
+  const long long rows = (long long)x.cache.pages * x.cache.Hk * x.cache.page_size;
+  if (!encode_cache(&tk, x.cache.k, rows, x.cache.d, fp8 ? 1 : 2, 16) ||
+      !encode_cache(&tv, x.cache.v, rows, x.cache.d, fp8 ? 1 : 2, 16))
+    return FA_ERR_CUDA;
+  // One CTA per SM, fewer where the longest possible sequences have fewer chunks.
+  const long long kt = ((long long)x.cache.max_pages * x.cache.page_size + kChunk - 1) / kChunk;
+  const long long rt = ((long long)x.max_new * G + a.tile_rows - 1) / a.tile_rows;
+  long long most = kt * rt;
+  most = most > kTreeCtas ? kTreeCtas : most * x.cache.Hk;
+  most = most > kTreeCtas ? kTreeCtas : most * x.cache.B;
+  const int ctas = (int)(most > kTreeCtas ? kTreeCtas : most);
+  const cudaStream_t s = static_cast<cudaStream_t>(x.stream);
+  note_launches(0);
+  const cudaError_t e = x.cache.d == 128 ? launch_small_d<128>(tk, tv, a, fp8, fp16, ctas, s)
+                                         : launch_small_d<64>(tk, tv, a, fp8, fp16, ctas, s);
+  if (e != cudaSuccess) return FA_ERR_CUDA;
+  if (kt > 1) {                                            // units of one chunk are never cut
+    const cudaError_t em = x.cache.d == 128 ? (fp16 ? launch_merge_d<128, true>(a, ctas, s) : launch_merge_d<128, false>(a, ctas, s))
+                                            : (fp16 ? launch_merge_d<64, true>(a, ctas, s) : launch_merge_d<64, false>(a, ctas, s));
+    if (em != cudaSuccess) return FA_ERR_CUDA;
+  }
+  note_launches(kt > 1 ? 2 : 1);
+  return FA_OK;
+}
+
+}  // extern "C"

@@ -47,13 +47,16 @@ typedef enum {
   FA_ERR_TIMEOUT = 4,       /* a kernel's bounded wait expired (reported by fa_check_status) */
   FA_ERR_WORKSPACE = 5,     /* workspace pointer NULL/misaligned or smaller than required   */
   FA_ERR_RANGE = 6          /* deterministic backward: a dQ partial was non-finite or too
-                               large for the fixed-point accumulator (fa_check_status)       */
+                               large for the fixed-point accumulator; paged cache: a page
+                               id, length or index that the cache cannot hold
+                               (fa_check_status)                                             */
 } fa_status;
 
 typedef enum {
   FA_BF16 = 0,
   FA_FP16 = 1,
-  FA_FP32 = 2              /* output type of fa_lse_merge only */
+  FA_FP32 = 2,             /* output type of fa_lse_merge only */
+  FA_E4M3 = 3              /* storage type of a paged cache only (fa_cache) */
 } fa_dtype;
 
 /* Largest sequence length accepted (tile lists live in shared memory: T <= 2048). */
@@ -205,8 +208,9 @@ int fa_bwd_splitq_choose(int B, int H, int N, int causal, int num_sms);
 
 /*
  * Synchronises `stream`, then reads and clears the device status word that kernels set
- * when a bounded wait expires (FA_ERR_TIMEOUT) or a deterministic backward meets a partial
- * outside its range (FA_ERR_RANGE).  Returns FA_OK, FA_ERR_TIMEOUT, FA_ERR_RANGE or
+ * when a bounded wait expires (FA_ERR_TIMEOUT), or when a deterministic backward meets a
+ * partial outside its range or a paged-cache call a page id, length or index outside its
+ * cache (FA_ERR_RANGE).  Returns FA_OK, FA_ERR_TIMEOUT, FA_ERR_RANGE or
  * FA_ERR_CUDA.  FA_ERR_CUDA also stands for a kernel that found its own launch state
  * unusable (its dynamic shared memory not 1024-byte aligned) and did no work; the device
  * records such states under codes of its own, which are never returned as they are.
@@ -375,6 +379,141 @@ typedef struct {
 
 size_t fa_fwd_fp8_workspace_bytes(int B, int H, int N, int d);
 int fa_fwd_fp8(const fa_fwd_fp8_args* args);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Paged key/value cache, and attention of new tokens over it (decoding, drafted trees, chunks).
+ *
+ * The pages leave the cache of generation to follow-on work ("边界条件", "局限与 Future Work");
+ * these entry points are the serving counterpart of the split-KV forward above: keys cut into
+ * ranges over the SMs and merged through their row max and sum.
+ *
+ * A cache holds K and V of B sequences in pages of page_size token rows, [pages, Hk, page_size,
+ * d] each: position p of sequence b and key head h is row p % page_size of [page_table[b][p /
+ * page_size], h].  Sequences may share pages that are only read.  Element types:
+ *   FA_BF16, FA_FP16 : the rows as they are;
+ *   FA_E4M3          : E4M3 codes and, for each row of d values, one E8M0 scale code (1 .. 247
+ *                      as fa_cache_append writes them), value = code * 2^(scale - 127).
+ * The lengths live on the device (lens[b]: positions held, cu_new[b] .. cu_new[b + 1]: the new
+ * tokens of sequence b among the call's `total`), so a captured graph can be replayed with other
+ * lengths.  What the host cannot see is checked by the kernels: a negative length, a position
+ * past max_pages, a page id that is no page or new-token bounds outside 0 .. total make
+ * fa_check_status return FA_ERR_RANGE; nothing outside the given buffers is read or written, and
+ * the results of the sequence concerned are undefined.
+ * ---------------------------------------------------------------------------------------
+ */
+typedef struct {
+  void* k; void* v;          /* [pages, Hk, page_size, d] of dtype, 16-byte aligned          */
+  uint8_t* k_scale;          /* [pages, Hk, page_size] E8M0 codes, 16-byte aligned; FA_E4M3  */
+  uint8_t* v_scale;          /* only, else NULL                                              */
+  const int32_t* page_table; /* device, [B, max_pages], rows table_stride apart              */
+  int pages, Hk, page_size, d;   /* page_size 16, 32, 64 or 128; d 64 or 128;
+                                    pages * Hk * page_size < 2^31                            */
+  int dtype;                 /* FA_BF16, FA_FP16 or FA_E4M3                                  */
+  int B, max_pages, table_stride;
+} fa_cache;
+
+/*
+ * Write new tokens' K and V rows behind what each sequence holds: token i of sequence b goes to
+ * position lens[b] + i.  A 16-bit cache takes the rows as they are (dtype must be the cache's).
+ * An E4M3 cache quantises each row of d values: e is the smallest exponent >= -126 with max |x| <=
+ * 448 * 2^e over the row's finite values, scale code e + 127, and each code is x * 2^-e rounded
+ * to the nearest E4M3 value (ties to even).  NaN and infinities become the NaN code (E4M3 has no
+ * infinity); magnitudes above 61440 (fp16) or 15 * 2^124 (bf16) are taken down to that, so that
+ * what is stored is finite in the source's type.
+ *   k_new, v_new : in, [total, Hk, d] (dtype), the d values contiguous, strides in elements and
+ *                  multiples of 8, 16-byte aligned (slices of a fused projection will do)
+ *   cu_new       : device int32 [B + 1], non-decreasing; tokens outside cu_new[0] ..
+ *                  cu_new[B] - 1 are ignored (a padded batch)
+ *   lens         : device int32 [B], positions held before the call (not changed)
+ * One launch.
+ */
+typedef struct {
+  fa_cache cache;
+  const void* k_new; const void* v_new;
+  long long k_token_stride, k_head_stride, v_token_stride, v_head_stride;
+  const int32_t* cu_new;
+  const int32_t* lens;
+  int total;
+  int dtype;
+  void* stream;
+} fa_cache_append_args;
+
+int fa_cache_append(const fa_cache_append_args* args);
+
+/*
+ * Read the cache back: k_out, v_out [B, Hk, N, d] of dtype (the cache's, or FA_BF16 or FA_FP16 of
+ * an E4M3 cache, each value rounded to nearest: exact in bf16), rows n < lens[b] of each sequence
+ * and zeros from there to N.  The layout is that of fa_fwd_partial's keys.  One launch.
+ */
+typedef struct {
+  fa_cache cache;
+  const int32_t* lens;
+  void* k_out; void* v_out;
+  int N;
+  int dtype;
+  void* stream;
+} fa_cache_read_args;
+
+int fa_cache_read(const fa_cache_read_args* args);
+
+/*
+ * Keep the accepted rows of drafted tokens: for i < counts[b], the row at position lens[b] +
+ * kept[b][i] moves to position lens[b] + i (codes and scales as they are).  kept[b] must be strictly
+ * increasing and not negative; a sequence whose list is not (or whose count is outside 0 ..
+ * width, or whose positions lie past the table) keeps all its rows and is reported as
+ * FA_ERR_RANGE.  The caller then adds counts to lens.  One launch.
+ *   kept   : device int32 [B, width];  counts : device int32 [B]
+ */
+typedef struct {
+  fa_cache cache;
+  const int32_t* lens;
+  const int32_t* kept;
+  const int32_t* counts;
+  int width;
+  void* stream;
+} fa_cache_keep_args;
+
+int fa_cache_keep(const fa_cache_keep_args* args);
+
+/*
+ * Attention of the new tokens over the cache, which already holds their own rows
+ * (fa_cache_append): query head hq of new token t of sequence b attends, in key head hq / (Hq /
+ * Hk), to positions p < lens[b] and to the new tokens j it may see at lens[b] + j:
+ *   tree_mask NULL : a chain, j <= t (one token: plain decoding; many: a chunk of a prompt)
+ *   tree_mask      : device uint64 [total, mask_words]; bit j % 64 of word j / 64 of token
+ *                    (cu_new[b] + t)'s row: whether it sees new token j of its sequence (itself
+ *                    included: nothing is seen that has no bit)
+ *   q       : in,  [total, Hq, d] (dtype), strides in elements, multiples of 8
+ *   o       : out, [total, Hq, d] (dtype), strides likewise; lse : out, fp32 [total, Hq], dense
+ *   max_new : at least every sequence's number of new tokens (a sequence with more is reported
+ *             as FA_ERR_RANGE); it and Hq / Hk choose the kernel
+ *   workspace : device scratch of fa_fwd_tree_workspace_bytes(total, Hq, Hk, d) bytes, 256-byte
+ *               aligned, needs no initialisation; calls that may run at the same time need
+ *               their own
+ * A row that sees no key gets O = 0 and LSE = -inf.  Keys and values that a row does not see do
+ * not enter its result, whatever they hold.  Tokens outside cu_new[0] .. cu_new[B] - 1 are left as
+ * they are in o and lse.  An E4M3 cache's values must be finite in dtype.  At most two launches.
+ */
+typedef struct {
+  fa_cache cache;
+  const void* q;
+  void* o;
+  float* lse;
+  long long q_token_stride, q_head_stride, o_token_stride, o_head_stride;
+  const int32_t* cu_new;
+  const int32_t* lens;
+  const uint64_t* tree_mask;
+  int mask_words;
+  int total, Hq, max_new;
+  int dtype;
+  float scale;
+  void* workspace; size_t workspace_bytes;
+  void* stream;
+} fa_fwd_tree_args;
+
+size_t fa_fwd_tree_workspace_bytes(int total, int Hq, int Hk, int d);
+int fa_fwd_tree(const fa_fwd_tree_args* args);
 
 /*
  * Diagnostic of failure detection (no counterpart in the pages).  Launches one small kernel
