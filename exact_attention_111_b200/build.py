@@ -15,7 +15,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfa.so")
 SOURCES = ["fa_host.cu", "fa_fwd.cu", "fa_bwd.cu", "fa_merge.cu", "fa_fwd_fp8.cu", "fa_selftest.cu", "fa_noalloc.cu",
-           "fa_cache.cu", "fa_tree.cu"]
+           "fa_cache.cu", "fa_tree.cu", "fa_tree_tc.cu"]
 HEADERS = ["fa_internal.h", "sm100.cuh", "fa_fp8.h", "fa_cache.cuh"]
 
 

@@ -102,6 +102,7 @@ __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t w) {
 
 constexpr int kChunk = 128;      // keys
 constexpr int kTreeCtas = 148;   // most CTAs (one per SM)
+constexpr int kBigRows = 256;    // rows of a unit of the tensor-memory kernel
 
 struct TreeArgs {
   CacheView c;
@@ -111,12 +112,13 @@ struct TreeArgs {
   const int* cu;                 // [B + 1]
   const int* lens;               // [B]
   const unsigned long long* mask;   // [total, words] or null
-  float* part_o;                 // [C, 2, tile_rows, d] partial sums of units cut between CTAs
-  float* part_ml;                // [C, 2, tile_rows, 2] their running max (log2 units) and sum
+  float* part_o;                 // [C, 2, slot_rows, d] partial sums of units cut between CTAs
+  float* part_ml;                // [C, 2, slot_rows, 2] their running max (log2 units) and sum
   int4* meta;                    // [C] what CTA c leaves to the merge
   long long q_tok, q_head, o_tok, o_head;   // strides in elements
   int total, Hq, G, words, max_new;
-  int tile_rows;                 // rows of a row tile (a multiple of G tokens' rows or of 16)
+  int tile_rows;                 // rows of a row tile
+  int slot_rows;                 // rows of a slot of part_o / part_ml: at least a unit's rows
   unsigned long long timeout_ns;
   float scale_log2;
 };
@@ -245,8 +247,12 @@ __device__ __forceinline__ void next_unit(const TreeArgs& a, Cursor& c) {
 int check_cache(const fa_cache& c);
 CacheView view_of(const fa_cache& c);
 // fa_host.cu: what fa_last_launch_count returns, and the TMA map of a cache's rows [rows][d] in
-// boxes of box_rows whole rows, 128-byte panels (64-byte rows for E4M3 at d = 64), swizzled.
+// boxes of box_rows rows, 128-byte panels (64-byte rows for E4M3 at d = 64), swizzled: a box holds all
+// panels (one after the other) or one.
 void note_launches(int n);
-bool encode_cache(CUtensorMap* m, const void* base, long long rows, int d, int elem, int box_rows);
+bool encode_cache(CUtensorMap* m, const void* base, long long rows, int d, int elem, int box_rows, bool all_panels);
+
+cudaError_t launch_tree_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp16, int ctas,
+                            cudaStream_t s);
 
 }  // namespace fa

@@ -226,12 +226,13 @@ int validate_bwd(const fa_bwd_args& x, bool check_workspace) {
 
 void note_launches(int n) { t_last_launches = n; }
 
-bool encode_cache(CUtensorMap* m, const void* base, long long rows, int d, int elem, int box_rows) {
+bool encode_cache(CUtensorMap* m, const void* base, long long rows, int d, int elem, int box_rows, bool all_panels) {
   if (!get_encode()) return false;
   const int row = d * elem, panel = row < 128 ? row : 128;
   const cuuint64_t dims[3] = {(cuuint64_t)(panel / elem), (cuuint64_t)rows, (cuuint64_t)(row / panel)};
   const cuuint64_t strides[2] = {(cuuint64_t)row, (cuuint64_t)panel};
-  const cuuint32_t box[3] = {(cuuint32_t)(panel / elem), (cuuint32_t)box_rows, (cuuint32_t)(row / panel)};
+  const cuuint32_t box[3] = {(cuuint32_t)(panel / elem), (cuuint32_t)box_rows,
+                             (cuuint32_t)(all_panels ? row / panel : 1)};
   const cuuint32_t estr[3] = {1, 1, 1};
   return g_encode(m, elem == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_UINT16, 3,
                   const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -574,9 +574,9 @@ __global__ void __launch_bounds__(256, 1)
                     pack2<kFp16>(o[mt][n][2 * hf] * inv, o[mt][n][2 * hf + 1] * inv);
             }
           } else {
-            float* pp = a.part_o + ((long long)slot * a.tile_rows + r) * D;
+            float* pp = a.part_o + ((long long)slot * a.slot_rows + r) * D;
             if (tq == 0) {
-              float* ml = a.part_ml + ((long long)slot * a.tile_rows + r) * 2;
+              float* ml = a.part_ml + ((long long)slot * a.slot_rows + r) * 2;
               ml[0] = m[mt][hf];
               ml[1] = lv;
             }
@@ -624,7 +624,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   float m = -INFINITY;
   for (int i = lane; i < n; i += 32) {
     const long long slot = i == 0 ? 2LL * c + 1 : 2LL * (c + i);
-    m = fmaxf(m, a.part_ml[(slot * a.tile_rows + r) * 2]);
+    m = fmaxf(m, a.part_ml[(slot * a.slot_rows + r) * 2]);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     float w = 0.f;
     if (i0 + lane < n) {
       const long long slot = i0 + lane == 0 ? 2LL * c + 1 : 2LL * (c + i0 + lane);
-      const float* ml = a.part_ml + (slot * a.tile_rows + r) * 2;
+      const float* ml = a.part_ml + (slot * a.slot_rows + r) * 2;
       w = ex2(ml[0] + neg);
       l += w * ml[1];
     }
@@ -643,7 +643,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
     for (int i = 0; i < k; ++i) {
       const float wi = __shfl_sync(0xffffffffu, w, i);
       const long long slot = i0 + i == 0 ? 2LL * c + 1 : 2LL * (c + i0 + i);
-      const float* p = a.part_o + (slot * a.tile_rows + r) * D + lane * kV;
+      const float* p = a.part_o + (slot * a.slot_rows + r) * D + lane * kV;
       if constexpr (kV == 4) {
         const float4 x = *reinterpret_cast<const float4*>(p);
         acc[0] += wi * x.x;
@@ -725,7 +725,7 @@ TreeLayout tree_layout(int rows, int d) {
 // Most rows a row tile can have in a call with this many new tokens.
 int most_rows(int total, int G) {
   const long long r = ((long long)total * G + 15) / 16 * 16;
-  return (int)(r < 32 ? r : 32);
+  return (int)(r < kBigRows ? r : kBigRows);
 }
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -787,12 +787,15 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   a.max_new = x.max_new;
   a.timeout_ns = 2000000000ull;
   a.scale_log2 = (float)((double)x.scale * 1.4426950408889634);
-  a.tile_rows = (long long)min(x.max_new, x.total) * G <= 16 ? 16 : 32;
+  const long long unit = (long long)min(x.max_new, x.total) * G;   // most rows of a key head
+  const bool big = unit > 32 && !fp8;
+  a.tile_rows = big ? kBigRows : unit <= 16 ? 16 : 32;
+  a.slot_rows = min(a.tile_rows, most_rows(x.total, G));
 
   CUtensorMap tk, tv;
   const long long rows = (long long)x.cache.pages * x.cache.Hk * x.cache.page_size;
-  if (!encode_cache(&tk, x.cache.k, rows, x.cache.d, fp8 ? 1 : 2, 16) ||
-      !encode_cache(&tv, x.cache.v, rows, x.cache.d, fp8 ? 1 : 2, 16))
+  if (!encode_cache(&tk, x.cache.k, rows, x.cache.d, fp8 ? 1 : 2, big ? x.cache.page_size : 16, !big) ||
+      !encode_cache(&tv, x.cache.v, rows, x.cache.d, fp8 ? 1 : 2, big ? x.cache.page_size : 16, !big))
     return FA_ERR_CUDA;
   // One CTA per SM, fewer where the longest possible sequences have fewer chunks.
   const long long kt = ((long long)x.cache.max_pages * x.cache.page_size + kChunk - 1) / kChunk;
@@ -803,7 +806,8 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   const int ctas = (int)(most > kTreeCtas ? kTreeCtas : most);
   const cudaStream_t s = static_cast<cudaStream_t>(x.stream);
   note_launches(0);
-  const cudaError_t e = x.cache.d == 128 ? launch_small_d<128>(tk, tv, a, fp8, fp16, ctas, s)
+  const cudaError_t e = big ? launch_tree_big(tk, tv, a, fp16, ctas, s)
+                        : x.cache.d == 128 ? launch_small_d<128>(tk, tv, a, fp8, fp16, ctas, s)
                                          : launch_small_d<64>(tk, tv, a, fp8, fp16, ctas, s);
   if (e != cudaSuccess) return FA_ERR_CUDA;
   if (kt > 1) {                                            // units of one chunk are never cut

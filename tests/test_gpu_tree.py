@@ -57,6 +57,13 @@ CASES = [
     ([0, 9], [20, 5], 21, 3, 128, 16, BF, True, "holes"),
     ([40], [100], 7, 1, 128, 128, HF, True, "chain"),
     ([5] * 40, [1, 2] * 20, 4, 2, 64, 16, BF, False, "tree"),
+    # many rows of a key head: several row tiles, units cut between CTAs
+    ([1000, 20, 0], [64, 129, 1], 16, 2, 128, 16, BF, False, "chain"),
+    ([700], [130], 12, 2, 64, 32, HF, False, "random"),
+    ([0, 513], [33, 64], 24, 3, 128, 128, HF, False, "tree"),
+    ([127, 128], [90, 91], 7, 1, 64, 128, BF, False, "holes"),
+    ([600, 3], [140, 70], 8, 2, 128, 64, HF, True, "tree"),
+    ([30, 400], [150, 64], 4, 1, 64, 16, BF, True, "chain"),
 ]
 
 
