@@ -92,6 +92,14 @@ __device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t w) {
   return r;
 }
 
+// bf16 queries meet an E4M3 cache's codes in fp16 products: a row is scaled by 2^k, which brings its
+// largest magnitude amax to [2^14, 2^15) (as far as k <= 112 does): the eight bits of a value are kept
+// down to 2^-28 of the largest, and below that the error stays under 2^-39 of it.
+__device__ __forceinline__ int row_factor(float amax) {
+  const int ex = static_cast<int>(__float_as_uint(amax) >> 23);      // biased exponent
+  return ex == 255 ? 0 : max(-113, min(112, 127 + 14 - ex));
+}
+
 // ------------------------------------------------------------------------------------
 // Schedule of the attention over the cache.  A unit is one (sequence, key head, row tile): rows are
 // the unit's (new token, query head of the group) pairs.  Its keys are cut into chunks of 128.
@@ -252,7 +260,7 @@ CacheView view_of(const fa_cache& c);
 void note_launches(int n);
 bool encode_cache(CUtensorMap* m, const void* base, long long rows, int d, int elem, int box_rows, bool all_panels);
 
-cudaError_t launch_tree_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp16, int ctas,
-                            cudaStream_t s);
+cudaError_t launch_tree_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp8, bool fp16,
+                            int ctas, cudaStream_t s);
 
 }  // namespace fa

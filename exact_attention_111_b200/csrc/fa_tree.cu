@@ -25,6 +25,7 @@ namespace fa {
 namespace {
 
 constexpr float kLn2f = 0.693147180559945309f;
+constexpr int kNoScale = -100000;        // no E yet: below every scale code
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -48,26 +49,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Two E4M3 codes in bytes 1 and 3 of x (the others zero) to two bf16: sign to bit 15, the seven
-// exponent and mantissa bits to bits 10..4, which reads as value * 2^-120 (bias 7 under bias 127;
-// E4M3's subnormals become bf16's); the product with 2^120 is exact.  The NaN code (all seven
-// bits set) would read as 480, so it is handled apart (see any_nan_code).
-__device__ __forceinline__ uint32_t codes_to_bf16x2(uint32_t x) {
-  const uint32_t r = (x & 0x80008000u) | ((x >> 4) & 0x07F007F0u);
-  __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&r);
-  const uint32_t k = 0x7B807B80u;                   // 2^120
-  v = __hmul2(v, *reinterpret_cast<const __nv_bfloat162*>(&k));
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-// Bytes (i, j) of w as two 16-bit floats.
-template <bool kFp16, int i, int j>
+// Bytes (i, j) of w, E4M3 codes, as two fp16.
+template <int i, int j>
 __device__ __forceinline__ uint32_t expand2(uint32_t w) {
-  if constexpr (kFp16) return e4m3_to_f16x2(__byte_perm(w, 0, i | (j << 4)));
-  else return codes_to_bf16x2(__byte_perm(w, 0, 4 | (i << 4) | (4 << 8) | (j << 12)));
-}
-// Whether one of the four codes is NaN (0x7F or 0xFF).
-__device__ __forceinline__ bool any_nan_code(uint32_t w) {
-  return ((((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u);
+  if constexpr (i == 0 && j == 1) return e4m3_to_f16x2(w);
+  else if constexpr (i == 2 && j == 3) return e4m3_to_f16x2(w >> 16);
+  else return e4m3_to_f16x2(__byte_perm(w, 0, i | (j << 4)));
 }
 
 template <int D, bool kFp8>
@@ -77,7 +64,7 @@ struct SmallCfg {
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kStages = kFp8 ? 20480 / kStage : 24576 / kStage;
   static constexpr int kRing = 8 * kStages * kStage;     // all warps
-  static constexpr int kSlot = 16 * D * 4 + 128;         // one warp's O, m and l of 16 rows
+  static constexpr int kSlot = 16 * D * 4 + 128 + 16;    // one warp's O, m and l of 16 rows, V's exponent
   static constexpr int kScales = kFp8 ? 8 * kStages * 32 : 0;
   static constexpr int kSmem = kRing + 4 * kSlot + kScales + 1024;
   // bytes between 16-byte chunks' rows: 128-byte panels (64-byte rows for E4M3 at d = 64)
@@ -91,12 +78,19 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
   else return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
+// kFp16: type of q and o.  A 16-bit cache's products are in that type.  An E4M3 cache's are in fp16, which
+// holds every code exactly: K's scale multiplies the score (32 bits), V's the probability before it
+// is rounded, p * 2^(e - E) with E a warp's own reference: 2^8 under the scales of its first keys,
+// moved (and O with it) when a scale is 2^15 above it.  So p * 2^(e - E) has fp16's full eleven
+// bits down to 2^-22 for keys of the usual scale, three more than bf16.  bf16 queries enter as fp16 with a
+// power of two for each row (row_factor).
 template <int D, bool kFp8, bool kFp16, int kMT>
 __global__ void __launch_bounds__(256, 1)
     tree_small_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const TreeArgs a) {
   using C = SmallCfg<D, kFp8>;
   constexpr int kNT = D / 8;                              // 8-column tiles of O
+  constexpr bool kMma16 = kFp8 || kFp16;                  // products in fp16
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint64_t full[8][C::kStages];
   __shared__ int abort_flag;
@@ -176,6 +170,7 @@ __global__ void __launch_bounds__(256, 1)
     // Q fragments; rows past the unit's last read the last one (never stored)
     uint32_t qf[kMT][D / 16][4];
     int tok[kMT][2];
+    float sl2[kMT][2];                                    // score factors of the lane's rows
 #pragma unroll
     for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
@@ -197,6 +192,29 @@ __global__ void __launch_bounds__(256, 1)
             qf[mt][kk][hf + 2] = *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 8 + 2 * tq);
           }
         }
+        sl2[mt][hf] = a.scale_log2;
+        if constexpr (kFp8 && !kFp16) {
+          float amax = 0.f;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const float2 f = unpack2<false>(qf[mt][kk][hf + i]);
+              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+          const int k = row_factor(amax);
+          const float f = scale_value(127 + k);
+          sl2[mt][hf] *= scale_value(127 - k);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int i = 0; i < 4; i += 2) {
+              const float2 v = unpack2<false>(qf[mt][kk][hf + i]);
+              qf[mt][kk][hf + i] = pack2<true>(v.x * f, v.y * f);
+            }
+        }
       }
     float o[kMT][kNT][4], m[kMT][2], l[kMT][2];
 #pragma unroll
@@ -208,6 +226,8 @@ __global__ void __launch_bounds__(256, 1)
       m[mt][0] = m[mt][1] = -INFINITY;
       l[mt][0] = l[mt][1] = 0.f;
     }
+
+    int eref = kNoScale;                                  // E4M3: E (as a scale code) of what O holds
 
     // ------------------------------------------------------------ the segment's steps
     bool more = true;
@@ -229,56 +249,47 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
               for (int i = 0; i < 4; ++i) sc[mt][j][i] = 0.f;
           float kf[2][2] = {{1.f, 1.f}, {1.f, 1.f}}, vf[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
-          uint32_t vh[2] = {0, 0};                        // fp16: scales of V's key pairs
-          bool odd = false;                               // a value in this lane's V codes is not finite
+          const bool masked = p0 + 16 > s.len;
           if constexpr (kFp8) {
             const uint8_t* sp = scales + stg * 32;
-            uint32_t nan_k = 0;                           // keys (rows of K) with a NaN code
 #pragma unroll
             for (int c = 0; c < D / 16; c += 2) {
               uint32_t kr[4];
               ldsm4(ak + swz<D, true>((lane & 7) + ((lane >> 3) & 1) * 8, c + (lane >> 4)), kr);
-              if constexpr (!kFp16)
-                nan_k |= (any_nan_code(kr[0]) || any_nan_code(kr[2]) ? 1u : 0u) |
-                         (any_nan_code(kr[1]) || any_nan_code(kr[3]) ? 2u : 0u);
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
-                const uint32_t a0 = expand2<kFp16, 0, 1>(kr[j]), a1 = expand2<kFp16, 2, 3>(kr[j]);
-                const uint32_t b0 = expand2<kFp16, 0, 1>(kr[2 + j]), b1 = expand2<kFp16, 2, 3>(kr[2 + j]);
+                const uint32_t a0 = expand2<0, 1>(kr[j]), a1 = expand2<2, 3>(kr[j]);
+                const uint32_t b0 = expand2<0, 1>(kr[2 + j]), b1 = expand2<2, 3>(kr[2 + j]);
 #pragma unroll
                 for (int mt = 0; mt < kMT; ++mt) {
-                  mma16816<kFp16>(sc[mt][j], qf[mt][c], a0, a1);
-                  mma16816<kFp16>(sc[mt][j], qf[mt][c + 1], b0, b1);
+                  mma16816<true>(sc[mt][j], qf[mt][c], a0, a1);
+                  mma16816<true>(sc[mt][j], qf[mt][c + 1], b0, b1);
                 }
               }
+            }
+            // the largest of V's scales among the keys that exist
+            const uint32_t top = __reduce_max_sync(0xffffffffu, lane < 16 && p0 + lane < s.len + s.T ? sp[16 + (lane & 15)] : 0u);
+            if ((int)top > eref + 15) {
+              const int e = (int)top - 8;
+              if (eref != kNoScale) {                     // rare: a first scale far above the ones before
+                const float f = exp2f((float)(eref - e));
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                  for (int n = 0; n < kNT; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
+              }
+              eref = e;
             }
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-              const uint32_t wk = *reinterpret_cast<const uint16_t*>(sp + 8 * j + 2 * tq);
-              const uint32_t wv = *reinterpret_cast<const uint16_t*>(sp + 16 + 8 * j + 2 * tq);
+              const int wk = *reinterpret_cast<const uint16_t*>(sp + 8 * j + 2 * tq);
+              const int wv = *reinterpret_cast<const uint16_t*>(sp + 16 + 8 * j + 2 * tq);
               kf[j][0] = scale_value(wk & 0xFF);
               kf[j][1] = scale_value(wk >> 8);
-              // bf16: P carries 2^e.  fp16: V does, down to 2^-24 (the type's last bit); P the rest
-              const int e0 = (int)(wv & 0xFF) - 127, e1 = (int)(wv >> 8) - 127;
-              if constexpr (kFp16) {
-                vh[j] = pack2<true>(scale_value(max(e0, -24) + 127), scale_value(max(e1, -24) + 127));
-                vf[j][0] = scale_value(min(e0 + 24, 0) + 127);
-                vf[j][1] = scale_value(min(e1 + 24, 0) + 127);
-              } else {
-                vf[j][0] = scale_value(wv & 0xFF);
-                vf[j][1] = scale_value(wv >> 8);
-              }
-            }
-            if constexpr (!kFp16) {
-              if (__any_sync(0xffffffffu, nan_k != 0)) {  // rare: a key that holds NaN scores NaN
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                  const unsigned bal = __ballot_sync(0xffffffffu, (nan_k >> j) & 1);
-#pragma unroll
-                  for (int i = 0; i < 2; ++i)
-                    if ((bal >> (4 * (2 * tq + i))) & 0xFu) kf[j][i] = __int_as_float(0x7FFFFFFF);
-                }
-              }
+              vf[j][0] = scale_value(max((wv & 0xFF) + 127 - eref, 0));
+              vf[j][1] = scale_value(max((wv >> 8) + 127 - eref, 0));
             }
           } else {
 #pragma unroll
@@ -293,7 +304,6 @@ __global__ void __launch_bounds__(256, 1)
             }
           }
           // ---- scale, mask, online softmax
-          const bool masked = p0 + 16 > s.len;
           uint32_t pf[kMT][4];
           unsigned see[kMT][2];                           // bit 2j + i: key 8j + 2 tq + i is visible
 #pragma unroll
@@ -305,7 +315,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
               for (int j = 0; j < 2; ++j)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) x[j][i] = sc[mt][j][2 * hf + i] * (kFp8 ? a.scale_log2 * kf[j][i] : a.scale_log2);
+                for (int i = 0; i < 2; ++i) x[j][i] = sc[mt][j][2 * hf + i] * (kFp8 ? sl2[mt][hf] * kf[j][i] : sl2[mt][hf]);
               if (masked) {
                 const int t = tok[mt][hf];
 #pragma unroll
@@ -357,7 +367,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
                   for (int i = 0; i < 2; ++i) p[j][i] = masked && !((see[mt][hf] >> (2 * j + i)) & 1) ? 0.f : p[j][i] * vf[j][i];
                 }
-                pf[mt][hf + 2 * j] = pack2<kFp16>(p[j][0], p[j][1]);
+                pf[mt][hf + 2 * j] = pack2<kMma16>(p[j][0], p[j][1]);
               }
             }
           }
@@ -369,35 +379,25 @@ __global__ void __launch_bounds__(256, 1)
             keep0 = (end > 0 ? 0xFFFFu : 0u) | (end > 1 ? 0xFFFF0000u : 0u);
             keep1 = (end > 8 ? 0xFFFFu : 0u) | (end > 9 ? 0xFFFF0000u : 0u);
           }
-          auto vfrag = [&](int c, uint32_t (&b)[4]) {      // V of columns 16 c .. 16 c + 15: two tiles
+          // V of columns 32 c .. 32 c + 31 (E4M3) or 16 c .. 16 c + 15: kVT tiles of 8 columns
+          constexpr int kVT = kFp8 ? 4 : 2;
+          auto vfrag = [&](int c, uint32_t (&b)[kVT][2]) {
             uint32_t vr[4];
             if constexpr (kFp8) {
-              // one chunk of 16 columns; lanes 16..31 fetch the same rows of the next chunk
-              ldsm4t(av + swz<D, true>((lane & 7) + ((lane >> 3) & 1) * 8, (c & ~1) + (lane >> 4)), vr);
-              const uint32_t lo8 = (c & 1) ? vr[2] : vr[0], hi8 = (c & 1) ? vr[3] : vr[1];
-              if constexpr (!kFp16) {
-                if (any_nan_code(lo8) || any_nan_code(hi8)) odd = true;
-              }
-              b[0] = expand2<kFp16, 0, 2>(lo8);
-              b[1] = expand2<kFp16, 0, 2>(hi8);
-              b[2] = expand2<kFp16, 1, 3>(lo8);
-              b[3] = expand2<kFp16, 1, 3>(hi8);
-              if constexpr (kFp16) {
+              ldsm4t(av + swz<D, true>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * c + (lane >> 4)), vr);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  __half2 x = *reinterpret_cast<__half2*>(&b[i]);
-                  x = __hmul2(x, *reinterpret_cast<const __half2*>(&vh[i & 1]));
-                  b[i] = *reinterpret_cast<uint32_t*>(&x);
-                }
+              for (int i = 0; i < 4; ++i) {               // keys 8 (i % 2) .., columns 16 (i / 2) ..
+                b[2 * (i >> 1)][i & 1] = expand2<0, 2>(vr[i]);
+                b[2 * (i >> 1) + 1][i & 1] = expand2<1, 3>(vr[i]);
               }
             } else {
               ldsm4t(av + swz<D, false>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * c + (lane >> 4)), vr);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) b[i] = vr[i];
+              for (int i = 0; i < 4; ++i) b[i >> 1][i & 1] = vr[i];
             }
           };
-          // The products one by one, visible keys only.  poison: only what NaN codes add.
-          auto one_by_one = [&](bool poison) {
+          // The products one by one, visible keys only.
+          auto one_by_one = [&]() {
             const int live = min(16, s.len + s.T - p0);
             for (int key = 0; key < live; ++key) {
               const int src = (lane & ~3) | ((key & 7) >> 1), j = key >> 3, i = key & 1;
@@ -407,12 +407,10 @@ __global__ void __launch_bounds__(256, 1)
               for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                  const float2 f = unpack2<kFp16>(__shfl_sync(0xffffffffu, j ? pf[mt][hf + 2] : pf[mt][hf], src));
+                  const float2 f = unpack2<kMma16>(__shfl_sync(0xffffffffu, j ? pf[mt][hf + 2] : pf[mt][hf], src));
                   w[mt][hf] = i ? f.y : f.x;
                   v[mt][hf] = (__shfl_sync(0xffffffffu, see[mt][hf], src) >> (2 * j + i)) & 1;
                 }
-              float sv = 1.f;
-              if constexpr (kFp8 && kFp16) sv = scale_value(max((int)scales[stg * 32 + 16 + key], 127 - 24));
 #pragma unroll
               for (int n = 0; n < kNT; ++n)
 #pragma unroll
@@ -420,9 +418,7 @@ __global__ void __launch_bounds__(256, 1)
                   float x;                                // V[key][column of accumulator (n, e)]
                   if constexpr (kFp8) {
                     const int col = 16 * (n >> 1) + 4 * tq + 2 * e + (n & 1);
-                    const uint32_t code = sk[C::kHalf + swz<D, true>(key, col >> 4) + (col & 15)];
-                    const bool nan = (code & 0x7F) == 0x7F;
-                    x = poison && !nan ? 0.f : nan ? __int_as_float(0x7FFFFFFF) : unpack2<true>(e4m3_to_f16x2(code)).x * sv;
+                    x = unpack2<true>(e4m3_to_f16x2(sk[C::kHalf + swz<D, true>(key, col >> 4) + (col & 15)])).x;
                   } else {
                     const int col = 8 * n + 2 * tq + e;
                     x = unpack2<kFp16>(*reinterpret_cast<const uint16_t*>(sk + C::kHalf + swz<D, false>(key, col >> 3) +
@@ -442,41 +438,35 @@ __global__ void __launch_bounds__(256, 1)
           if (masked) {
             bool bad = false;
 #pragma unroll
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t b[4];
+            for (int c = 0; c < kNT / kVT; ++c) {
+              uint32_t b[kVT][2];
               vfrag(c, b);
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const uint32_t w = b[i] & ((i & 1) ? keep1 : keep0);
-                const uint32_t e = kFp16 ? 0x7C00u : 0x7F80u;
+              for (int i = 0; i < 2 * kVT; ++i) {
+                const uint32_t w = b[i >> 1][i & 1] & ((i & 1) ? keep1 : keep0);
+                const uint32_t e = kMma16 ? 0x7C00u : 0x7F80u;
                 bad |= (w & e) == e || ((w >> 16) & e) == e;
               }
             }
-            apart = __any_sync(0xffffffffu, bad || odd);
-            odd = false;
+            apart = __any_sync(0xffffffffu, bad);
           }
           if (apart) {
-            one_by_one(false);
+            one_by_one();
           } else {
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            uint32_t b[4];
-            vfrag(c, b);
-            if (masked) {
-              b[0] &= keep0;
-              b[1] &= keep1;
-              b[2] &= keep0;
-              b[3] &= keep1;
-            }
+            for (int c = 0; c < kNT / kVT; ++c) {
+              uint32_t b[kVT][2];
+              vfrag(c, b);
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt) {
-              mma16816<kFp16>(o[mt][2 * c], pf[mt], b[0], b[1]);
-              mma16816<kFp16>(o[mt][2 * c + 1], pf[mt], b[2], b[3]);
+              for (int i = 0; i < kVT; ++i) {
+                if (masked) {
+                  b[i][0] &= keep0;
+                  b[i][1] &= keep1;
+                }
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) mma16816<kMma16>(o[mt][kVT * c + i], pf[mt], b[i][0], b[i][1]);
+              }
             }
-          }
-          if constexpr (kFp8 && !kFp16) {                 // NaN codes went in as numbers
-            if (__any_sync(0xffffffffu, odd)) one_by_one(true);
-          }
           }
         }
         ++used;
@@ -497,6 +487,7 @@ __global__ void __launch_bounds__(256, 1)
         l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
         l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
       }
+      int em = eref;                                      // E of this row block's O
       for (int half = 4; half > 0; half >>= 1) {
         __syncthreads();
         if (warp >= half && warp < 2 * half) {
@@ -511,13 +502,20 @@ __global__ void __launch_bounds__(256, 1)
             sm[16 + r0] = l[mt][0];
             sm[24 + r0] = l[mt][1];
           }
+          if (kFp8 && lane == 0) reinterpret_cast<int*>(sm)[32] = em;
         }
         __syncthreads();
         if (warp < half) {
           const uint8_t* sl = slots + warp * C::kSlot;
           const float4* so = reinterpret_cast<const float4*>(sl);
           const float* sm = reinterpret_cast<const float*>(sl + 16 * D * 4);
-          float fa[2], fb[2];
+          float fa[2], fb[2], ga = 1.f, gb = 1.f;         // factors of O beside the maxima's
+          if constexpr (kFp8) {
+            const int eb = reinterpret_cast<const int*>(sm)[32], en = max(em, eb);
+            ga = exp2f((float)(em - en));
+            gb = exp2f((float)(eb - en));
+            em = en;
+          }
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const float mb = sm[r0 + 8 * hf], lb = sm[16 + r0 + 8 * hf];
@@ -527,6 +525,8 @@ __global__ void __launch_bounds__(256, 1)
             fb[hf] = ex2(mb + neg);
             m[mt][hf] = mn;
             l[mt][hf] = l[mt][hf] * fa[hf] + lb * fb[hf];
+            fa[hf] *= ga;
+            fb[hf] *= gb;
           }
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
@@ -538,6 +538,7 @@ __global__ void __launch_bounds__(256, 1)
           }
         }
       }
+      if (mt == kMT - 1) eref = em;
     }
 
     // ------------------------------------------------------------ results
@@ -554,8 +555,10 @@ __global__ void __launch_bounds__(256, 1)
           const int r = mt * 16 + hf * 8 + r0;
           if (r >= nrows) continue;
           const float lv = l[mt][hf];
+          // what O is a multiple of: 2^(E - 127)
+          const float vref = kFp8 && eref != kNoScale ? exp2f((float)(eref - 127)) : 1.f;
           if (whole) {
-            const float inv = lv == 0.f ? 0.f : 1.f / lv;
+            const float inv = lv == 0.f ? 0.f : vref / lv;
             const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
             const long long tk = s.cu0 + t;
             const int hq = h * a.G + g;
@@ -584,8 +587,8 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
               for (int c = 0; c < D / 16; ++c)
                 *reinterpret_cast<float4*>(pp + 16 * c + 4 * tq) =
-                    make_float4(o[mt][2 * c][2 * hf], o[mt][2 * c + 1][2 * hf], o[mt][2 * c][2 * hf + 1],
-                                o[mt][2 * c + 1][2 * hf + 1]);
+                    make_float4(o[mt][2 * c][2 * hf] * vref, o[mt][2 * c + 1][2 * hf] * vref,
+                                o[mt][2 * c][2 * hf + 1] * vref, o[mt][2 * c + 1][2 * hf + 1] * vref);
             } else {
 #pragma unroll
               for (int n = 0; n < kNT; ++n)
@@ -788,7 +791,7 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   a.timeout_ns = 2000000000ull;
   a.scale_log2 = (float)((double)x.scale * 1.4426950408889634);
   const long long unit = (long long)min(x.max_new, x.total) * G;   // most rows of a key head
-  const bool big = unit > 32 && !fp8;
+  const bool big = unit > 32;
   a.tile_rows = big ? kBigRows : unit <= 16 ? 16 : 32;
   a.slot_rows = min(a.tile_rows, most_rows(x.total, G));
 
@@ -806,7 +809,7 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   const int ctas = (int)(most > kTreeCtas ? kTreeCtas : most);
   const cudaStream_t s = static_cast<cudaStream_t>(x.stream);
   note_launches(0);
-  const cudaError_t e = big ? launch_tree_big(tk, tv, a, fp16, ctas, s)
+  const cudaError_t e = big ? launch_tree_big(tk, tv, a, fp8, fp16, ctas, s)
                         : x.cache.d == 128 ? launch_small_d<128>(tk, tv, a, fp8, fp16, ctas, s)
                                          : launch_small_d<64>(tk, tv, a, fp8, fp16, ctas, s);
   if (e != cudaSuccess) return FA_ERR_CUDA;

@@ -27,13 +27,14 @@ namespace {
 
 constexpr float kLn2f = 0.693147180559945309f;
 
-template <int D>
+template <int D, bool kFp8>
 struct BigCfg {
   static constexpr int kPanels = D / 64;
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int kPanelBytes = kTile * 128;
   static constexpr int kStages = D == 64 ? 4 : 2;
-  static constexpr int kSmem = 2 * kTileBytes + 2 * kStages * kTileBytes + 1024;
+  static constexpr int kCodes = kTile * D;                // one tile's E4M3 codes
+  static constexpr int kSmem = 2 * kTileBytes + 2 * kStages * kTileBytes + (kFp8 ? 2 * kCodes : 0);
   static constexpr int kOCol = 256;
   static constexpr int kCorrWarp = 8, kLoadWarp = 12, kMmaWarp = 13;
   // 512 threads x 128 registers at launch, shared out again by setmaxnreg: the shares add up to
@@ -44,51 +45,70 @@ struct BigCfg {
   static constexpr int kPolyOf8 = D == 64 ? 2 : 0;
 };
 
+// A segment: the CTA's run of tiles [kt0, kt0 + n) of one unit; nu of them can be seen by some row.
+struct Seg {
+  long long g;                   // first chunk in the line
+  SeqView s;
+  int b, h, unit, row0, nrows, kt0, n, nu;
+  bool from_start, to_end;
+};
+
+// A walk over the CTA's segments.
+struct Walk {
+  Cursor c;
+  long long g;
+  int left;
+  Seg e;
+  __device__ __forceinline__ void start(const Cursor& c0, const Part& p) {
+    c = c0;
+    g = p.lo;
+    left = p.n;
+  }
+  __device__ __forceinline__ bool next(const TreeArgs& a) {
+    if (left <= 0) return false;
+    e.s = c.s;
+    e.b = c.b;
+    e.h = c.h;
+    e.unit = c.u;
+    e.row0 = (c.u - c.h * c.s.RT) * a.tile_rows;
+    e.nrows = (int)min((long long)a.tile_rows, (long long)c.s.T * a.G - e.row0);
+    e.kt0 = c.kt;
+    e.n = min(c.s.KT - c.kt, left);
+    e.nu = max(0, min(e.n, c.last / kChunk + 1 - c.kt));
+    e.from_start = c.kt == 0;
+    e.to_end = c.kt + e.n == c.s.KT;
+    e.g = g;
+    g += e.n;
+    left -= e.n;
+    if (left > 0) next_unit(a, c);
+    return true;
+  }
+};
+
 struct BigShared {
   uint64_t q_full[2], o_full[2];
   uint64_t k_full[4], v_full[4], k_empty[4], v_empty[4], v_ok[4];
   uint64_t s_full[2], p_full[2], alpha_full[2], o_ready[2];
+  uint64_t c_full[2], c_empty[2];       // E4M3: staged codes of K and of V
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  // [group][its segments mod 2]: number + 1 of a segment where a new token's value was not finite.
-  // Entry n + 2 of a group is written only after the group's softmax began segment n + 1.
-  int odd[2][2];
+  // [group][its segments mod 8]: number + 1 of a segment where a new token's value was not finite.  Who
+  // writes them is at most kStages + 1 tiles, so 5 segments, ahead of the slower softmax group.
+  int odd[2][8];
   float alpha[2][kTile];
+  // E4M3: staged scale codes of a tile, and by tile mod 8 the factors of its K, of what O holds and
+  // of O (see the converter).  Entry u is written again for tile u + 8, whose K slot is free only
+  // after S of tile u + 8 - kStages, so of u + 4, which waited for both softmax groups to have finished u + 3.
+  alignas(16) uint8_t scales[2][kTile];
+  float kfac[8], vfac[8], vref[8];
+  Walk walk[8];                  // one per softmax warp, whose registers are full
 };
 
 template <int N>
 __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N>
 __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
-// A segment: the CTA's run of tiles [kt0, kt0 + n) of one unit; nu of them can be seen by some row.
-struct Seg {
-  SeqView s;
-  int b, h, unit, row0, nrows, kt0, n, nu;
-  bool from_start, to_end;
-  long long g;                   // first chunk in the line
-};
-
-__device__ __forceinline__ Seg take_segment(const TreeArgs& a, Cursor& c, long long& g, int& left) {
-  Seg e;
-  e.s = c.s;
-  e.b = c.b;
-  e.h = c.h;
-  e.unit = c.u;
-  e.row0 = (c.u - c.h * c.s.RT) * a.tile_rows;
-  e.nrows = (int)min((long long)a.tile_rows, (long long)c.s.T * a.G - e.row0);
-  e.kt0 = c.kt;
-  e.n = min(c.s.KT - c.kt, left);
-  e.nu = max(0, min(e.n, c.last / kChunk + 1 - c.kt));
-  e.from_start = c.kt == 0;
-  e.to_end = c.kt + e.n == c.s.KT;
-  e.g = g;
-  g += e.n;
-  left -= e.n;
-  if (left > 0) next_unit(a, c);
-  return e;
-}
 
 // Whether tile kt holds new tokens or reaches past them.
 __device__ __forceinline__ bool tail_tile(const Seg& e, int kt) { return (kt + 1) * kChunk > e.s.len; }
@@ -116,17 +136,227 @@ __device__ __forceinline__ uint32_t visible32(const TreeArgs& a, const SeqView& 
   return k < 32 ? v & ((1u << k) - 1u) : v;
 }
 
-template <int D, bool kFp16>
+// E4M3 rows enter the fp16 products as code * 2^(scale - E): a code is exact in fp16, and with E the
+// largest scale of the tile's keys what a row of a much smaller scale loses is below 2^-25 of the
+// largest, far under the products' own rounding.  K: E is the tile's, its 2^E goes into the
+// tile's score factor.  V: O adds up tiles, so E stays the segment's (its first tile's) while later
+// tiles' scales are at most 2^7 larger (448 * 2^7 is the last that fp16 holds); one that is larger
+// becomes E, and what O holds is scaled down with the softmax's own rescale.
+//
+// Three warps (12, 14, 15; 96 threads).  Warp 12 keeps one tile's codes of K and of V ahead in shared
+// memory by TMA, all three expand them into the ring's tiles.  In tiles that hold new tokens V's rows
+// past the end become zero and so do NaN codes, noted (see the top of the file).
+template <int D, bool kFp8, bool kFp16>
+__device__ void convert_role(const TreeArgs& a, BigShared& sh, uint8_t* sK, uint8_t* sV, uint8_t* sC,
+                             const CUtensorMap* tm_k, const CUtensorMap* tm_v, Walk& w, const Cursor& cur,
+                             const Part& part) {
+  using C = BigCfg<D, kFp8>;
+  constexpr int kLanes = D / 16;                          // 16-code chunks of a row
+  const int lane = lane_id();
+  const bool loader = warp_id() == C::kLoadWarp;
+  const int ci = loader ? lane : 32 + (warp_id() - C::kMmaWarp - 1) * 32 + lane;
+  const DevStatus st{a.c.status, a.timeout_ns};
+  volatile int* abort_flag = &sh.abort_flag;
+  const int R = 1 << a.c.page_shift, boxes = kTile / R;
+  const int chunk = ci % kLanes, row0 = ci / kLanes;
+  const Seg& e = w.e;
+
+  // ---- staging (warp 12): tile nl's codes, K's with both sets of scale codes
+  Walk lw;
+  int lu = 0, nl[2] = {0, 0};
+  bool more = false, ok = true;
+  if (loader) {
+    lw.start(cur, part);
+    do more = lw.next(a); while (more && lw.e.nu == 0);
+    if (lane == 0) {
+      prefetch_tmap(tm_k);
+      prefetch_tmap(tm_v);
+    }
+  }
+  auto stage = [&](int which) {                           // K (0) then V (1) of the loader's tile
+    if (!loader || !more || !ok) return;
+    if (nl[which] > 0) ok = mbar_wait(&sh.c_empty[which], (nl[which] - 1) & 1, abort_flag, st);
+    if (!__all_sync(0xffffffffu, ok)) { ok = false; return; }
+    const int pos = (lw.e.kt0 + lu) * kChunk + lane * R;
+    int row = (int)((long long)a.c.pages * a.c.Hk << a.c.page_shift);   // behind the last row: zeros
+    bool valid = false;
+    if (lane < boxes && pos < lw.e.s.len + lw.e.s.T) {
+      const long long r = slot_row(a.c, lw.e.b, lw.e.h, pos);
+      if (r >= 0) {
+        row = (int)r;
+        valid = true;
+      }
+    }
+    const int nvalid = __popc(__ballot_sync(0xffffffffu, valid));
+    if (lane == 0) mbar_arrive_expect_tx(&sh.c_full[which], C::kCodes + (which == 0 ? 2 * nvalid * R : 0));
+    __syncwarp();
+    if (lane < boxes) {
+      tma_load_3d(sC + which * C::kCodes + lane * R * D, which == 0 ? tm_k : tm_v, &sh.c_full[which], 0, row, 0);
+      if (which == 0 && valid) {
+        bulk_load(&sh.scales[0][lane * R], a.c.ks + row, R, &sh.c_full[0]);
+        bulk_load(&sh.scales[1][lane * R], a.c.vs + row, R, &sh.c_full[0]);
+      }
+    }
+    ++nl[which];
+    if (which == 1 && ++lu >= lw.e.nu) {
+      lu = 0;
+      do more = lw.next(a); while (more && lw.e.nu == 0);
+    }
+    __syncwarp();
+  };
+  stage(0);
+  stage(1);
+
+  int n = 0;                                              // tiles converted
+  int seg[2] = {0, 0};
+  uint32_t eref = 0;
+  while (ok && w.next(a)) {
+    const int nq = e.nrows > kTile ? 2 : 1;
+    for (int u = 0; u < e.nu && ok; ++u, ++n) {
+      const int kt = e.kt0 + u;
+      const int keys = min(kTile, e.s.len + e.s.T - kt * kChunk);
+      const bool tail = tail_tile(e, kt);
+      const int s = n % C::kStages;
+      const uint32_t ph = ((n / C::kStages) - 1) & 1;
+      uint32_t sv[(kTile * kLanes + 95) / 96 / 4 + 1];    // V scale codes of this thread's rows
+      uint32_t ek = 0;
+#pragma unroll
+      for (int which = 0; which < 2; ++which) {
+        ok = mbar_wait(&sh.c_full[which], n & 1, abort_flag, st);
+        if (ok && n >= C::kStages) ok = mbar_wait(which == 0 ? &sh.k_empty[s] : &sh.v_empty[s], ph, abort_flag, st);
+        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+        if (which == 0) {
+          // the largest scale codes of K and V among the keys that exist
+          uint32_t x = *reinterpret_cast<const uint32_t*>(&sh.scales[0][4 * lane]);
+          uint32_t y = *reinterpret_cast<const uint32_t*>(&sh.scales[1][4 * lane]);
+          const int k = keys - 4 * lane;
+          const uint32_t keep = k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
+          x &= keep;
+          y &= keep;
+          x = max(max(x & 0xFF, (x >> 8) & 0xFF), max((x >> 16) & 0xFF, x >> 24));
+          y = max(max(y & 0xFF, (y >> 8) & 0xFF), max((y >> 16) & 0xFF, y >> 24));
+          ek = __reduce_max_sync(0xffffffffu, x);
+          const uint32_t ev = __reduce_max_sync(0xffffffffu, y);
+          float vfac = 1.f;
+          if (u == 0) {
+            eref = ev;
+          } else if (ev > eref + 7) {
+            vfac = exp2f((float)eref - (float)ev);
+            eref = ev;
+          }
+          if (ci == 0) {
+            *reinterpret_cast<volatile float*>(&sh.kfac[n & 7]) = scale_value(ek);
+            *reinterpret_cast<volatile float*>(&sh.vfac[n & 7]) = vfac;
+            *reinterpret_cast<volatile float*>(&sh.vref[n & 7]) = scale_value(eref);
+          }
+        }
+        uint8_t* dst0 = (which == 0 ? sK : sV) + s * C::kTileBytes;
+        const uint8_t* src0 = sC + which * C::kCodes;
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < (kTile * kLanes + 95) / 96; ++i) {
+          const int r = row0 + i * (96 / kLanes);
+          if (r < kTile) {
+            uint4 x = *reinterpret_cast<const uint4*>(
+                src0 + (D == 64 ? r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4) : r * 128 + ((chunk ^ (r & 7)) << 4)));
+            // V's scale codes are staged with K's: keep this thread's before K's staging is released
+            uint32_t code;
+            if (which == 0) {
+              code = sh.scales[0][r];
+              if ((i & 3) == 0) sv[i >> 2] = 0;
+              sv[i >> 2] |= (uint32_t)sh.scales[1][r] << (8 * (i & 3));
+            } else {
+              code = (sv[i >> 2] >> (8 * (i & 3))) & 0xFF;
+              if (tail) {
+                if (r >= keys) {
+                  x = make_uint4(0, 0, 0, 0);
+                  code = 0;
+                }
+                uint32_t* y = &x.x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {             // NaN codes: 0x7F + 1 carries into bit 7
+                  const uint32_t b = ((y[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+                  if (b != 0) {
+                    y[j] &= ~((b >> 7) * 0xFFu);
+                    odd = true;
+                  }
+                }
+              }
+            }
+            const int d = max((int)code - (int)(which == 0 ? ek : eref), -24);
+            const uint32_t f1 = pack2<true>(scale_value(127 + min(d, 15)), 0.f) & 0xFFFFu;
+            const uint32_t f = f1 | (f1 << 16);
+            uint32_t o[8];
+            const uint32_t* y = &x.x;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const uint32_t h = e4m3_to_f16x2((j & 1) ? y[j >> 1] >> 16 : y[j >> 1]);
+              const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&f));
+              o[j] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            // the row's 16-byte chunks 2 chunk, 2 chunk + 1; half of the lanes start with the
+            // second, so that a quarter warp's stores hit all banks
+            uint8_t* dst = dst0 + r * 128 + (chunk >> 2) * C::kPanelBytes;
+            const int c0 = (2 * chunk) & 7, sw = D == 128 ? (chunk >> 2) & 1 : 0;
+            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<uint4*>(dst + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
+          }
+        }
+        if (odd)
+          for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 7]) = seg[q] + 1;
+        fence_async_smem();
+        mbar_arrive(which == 0 ? &sh.k_full[s] : &sh.v_full[s]);
+        mbar_arrive(&sh.c_empty[which]);
+        stage(which);
+      }
+    }
+    if (e.nu > 0)
+      for (int q = 0; q < nq; ++q) ++seg[q];
+  }
+  // After a wait that ran out: copies in flight land before the shared memory goes away.
+  if (*abort_flag && loader && lane == 0)
+    for (int i = 0; i < 2; ++i)
+      if (nl[i] > 0) mbar_wait_drain(&sh.c_full[i], (nl[i] - 1) & 1, st);
+  __syncwarp();
+}
+
+// A Q row of bf16 pairs to fp16 (row_factor).  Returns the inverse factor, for the scores.
+template <int N>
+__device__ __forceinline__ float row_to_fp16(uint32_t* x) {
+  float amax = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 f = unpack2<false>(x[i]);
+    amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
+  }
+  const int k = row_factor(amax);
+  const float f = scale_value(127 + k);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float2 v = unpack2<false>(x[i]);
+    x[i] = pack2<true>(v.x * f, v.y * f);
+  }
+  return scale_value(127 - k);
+}
+
+// kFp16: type of q and o.  The products of a 16-bit cache are in that type, those of an E4M3 cache in fp16.
+template <int D, bool kFp8, bool kFp16>
 __global__ void __launch_bounds__(512, 1)
     tree_big_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                     const TreeArgs a) {
-  using C = BigCfg<D>;
+  using C = BigCfg<D, kFp8>;
+  constexpr bool kMmaFp16 = kFp8 || kFp16;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ BigShared sh;
-  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
-  uint8_t* sQ = smem_raw + pad;
+  if ((smem_addr(smem_raw) & 1023u) != 0) {               // the tiles' swizzle needs it
+    if (threadIdx.x == 0) atomicCAS(a.c.status, 0, kDevBadState);
+    return;
+  }
+  uint8_t* sQ = smem_raw;
   uint8_t* sK = sQ + 2 * C::kTileBytes;
   uint8_t* sV = sK + C::kStages * C::kTileBytes;
+  uint8_t* sC = sV + C::kStages * C::kTileBytes;          // E4M3: staged codes of K, then of V
   const int warp = warp_id(), lane = lane_id();
   const DevStatus st{a.c.status, a.timeout_ns};
   volatile int* abort_flag = &sh.abort_flag;
@@ -134,8 +364,8 @@ __global__ void __launch_bounds__(512, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&sh.k_full[s], 1);
-      mbar_init(&sh.v_full[s], 1);
+      mbar_init(&sh.k_full[s], kFp8 ? 96 : 1);
+      mbar_init(&sh.v_full[s], kFp8 ? 96 : 1);
       mbar_init(&sh.k_empty[s], 1);
       mbar_init(&sh.v_empty[s], 1);
       mbar_init(&sh.v_ok[s], 128);
@@ -147,7 +377,11 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&sh.p_full[q], 128);
       mbar_init(&sh.alpha_full[q], 128);
       mbar_init(&sh.o_ready[q], 128);
-      sh.odd[q][0] = sh.odd[q][1] = 0;
+      for (int i = 0; i < 8; ++i) sh.odd[q][i] = 0;
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh.c_full[i], 1);
+      mbar_init(&sh.c_empty[i], 96);
     }
     mbar_init(&sh.mma_done, 1);
     sh.abort_flag = 0;
@@ -162,8 +396,6 @@ __global__ void __launch_bounds__(512, 1)
   if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
   Cursor cur{};
   if (part.n > 0) cur = locate(a, part.lo);
-  long long g = part.lo;
-  int left = part.n;
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -171,7 +403,12 @@ __global__ void __launch_bounds__(512, 1)
 
   if (warp >= C::kLoadWarp) {
     reg_dec<C::kRegOther>();
-    if (warp == C::kLoadWarp) {
+    Walk w;
+    w.start(cur, part);
+    const Seg& e = w.e;
+    if (warp != C::kMmaWarp && kFp8) {
+      convert_role<D, kFp8, kFp16>(a, sh, sK, sV, sC, &tm_k, &tm_v, w, cur, part);
+    } else if (warp == C::kLoadWarp) {
       // ---------------------------------------------------------------- producer
       const int R = 1 << a.c.page_shift;                  // rows per box: one page
       const int boxes = kTile / R;
@@ -181,8 +418,7 @@ __global__ void __launch_bounds__(512, 1)
         prefetch_tmap(&tm_k);
         prefetch_tmap(&tm_v);
       }
-      while (left > 0 && ok) {
-        const Seg e = take_segment(a, cur, g, left);
+      while (ok && w.next(a)) {
         const int end = e.s.len + e.s.T;
         for (int u = 0; u < e.nu && ok; ++u) {
           const int s = nk % C::kStages;
@@ -223,16 +459,15 @@ __global__ void __launch_bounds__(512, 1)
     } else if (warp == C::kMmaWarp) {
       // ---------------------------------------------------------------- MMA issuer
       if (lane == 0) {
-        const uint32_t idesc_s = idesc_f16(128, 128, kFp16, false, false);
-        const uint32_t idesc_pv = idesc_f16(128, D, kFp16, false, true);
+        const uint32_t idesc_s = idesc_f16(128, 128, kMmaFp16, false, false);
+        const uint32_t idesc_pv = idesc_f16(128, D, kMmaFp16, false, true);
         const uint32_t aQ = smem_addr(sQ), aK = smem_addr(sK), aV = smem_addr(sV);
         int nt = 0;                                       // tiles before this segment
         int np[2] = {0, 0};                               // P tiles consumed
         uint32_t tails = 0;                               // bit s: parity of stage s's safe V tiles
         uint32_t nseg[2] = {0, 0};
         bool ok = true;
-        while (left > 0 && ok) {
-          const Seg e = take_segment(a, cur, g, left);
+        while (ok && w.next(a)) {
           const int nq = e.nrows > kTile ? 2 : 1;
           for (int u = 0; u <= e.nu && ok && e.nu > 0; ++u) {
             const int tp = nt + u - 1, tc = nt + u;
@@ -242,7 +477,7 @@ __global__ void __launch_bounds__(512, 1)
               if (u == 0 || q >= nq) return true;
               if (!v_ready) {
                 if (!mbar_wait(&sh.v_full[sp], (tp / C::kStages) & 1, abort_flag, st)) return false;
-                if (tail_tile(e, e.kt0 + u - 1)) {
+                if (!kFp8 && tail_tile(e, e.kt0 + u - 1)) {
                   if (!mbar_wait(&sh.v_ok[sp], (tails >> sp) & 1u, abort_flag, st)) return false;
                   tails ^= 1u << sp;
                 }
@@ -303,12 +538,14 @@ __global__ void __launch_bounds__(512, 1)
     int nt = 0, cq[2] = {0, 0};
     int seg[2] = {0, 0};
     bool ok = true;
-    while (left > 0 && ok) {
-      const Seg e = take_segment(a, cur, g, left);
+    Walk w;
+    w.start(cur, part);
+    const Seg& e = w.e;
+    while (ok && w.next(a)) {
       const int nq = e.nrows > kTile ? 2 : 1;
       for (int u = 0; u < e.nu && ok; ++u) {
         const int kt = e.kt0 + u;
-        if (tail_tile(e, kt)) {
+        if (!kFp8 && tail_tile(e, kt)) {
           // this thread's V row (key): zero past the end, and where it is not finite
           const int t = nt + u, s = t % C::kStages;
           ok = mbar_wait(&sh.v_full[s], (t / C::kStages) & 1, abort_flag, st);
@@ -319,18 +556,18 @@ __global__ void __launch_bounds__(512, 1)
           for (int c = 0; c < D / 8; ++c) {
             uint4* p = reinterpret_cast<uint4*>(vrow + (c >> 3) * C::kPanelBytes + (((c & 7) ^ (r & 7)) << 4));
             uint4 x = past ? make_uint4(0, 0, 0, 0) : *p;
-            uint32_t* w = &x.x;
+            uint32_t* y = &x.x;
             bool odd = past;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               constexpr uint32_t ex = kFp16 ? 0x7C00u : 0x7F80u;
-              if ((w[i] & ex) == ex) { w[i] &= 0xFFFF0000u; odd = true; }
-              if (((w[i] >> 16) & ex) == ex) { w[i] &= 0xFFFFu; odd = true; }
+              if ((y[i] & ex) == ex) { y[i] &= 0xFFFF0000u; odd = true; }
+              if (((y[i] >> 16) & ex) == ex) { y[i] &= 0xFFFFu; odd = true; }
             }
             if (odd) {
               *p = x;
               if (!past)
-                for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 1]) = seg[q] + 1;
+                for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 7]) = seg[q] + 1;
             }
           }
           fence_async_smem();
@@ -377,25 +614,37 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
     const uint32_t tS = tmem + q * 128 + lane_off;
     const uint32_t tO = tmem + C::kOCol + q * D + lane_off;
-    const float sl2 = a.scale_log2;
     int cs = 0, nseg = 0;
+    int tile = 0;                                         // tiles of the CTA before this segment
     bool ok = true;
-    while (left > 0 && ok) {
-      const Seg e = take_segment(a, cur, g, left);
+    Walk& w = sh.walk[warp];
+    if (lane == 0) w.start(cur, part);
+    const Seg& e = w.e;
+    while (ok) {
+      __syncwarp();
+      bool more = false;
+      if (lane == 0) more = w.next(a);
+      if (!__shfl_sync(0xffffffffu, more, 0)) break;
+      __syncwarp();
+      const int tile0 = tile;
+      tile += e.nu;
       if (q == 1 && e.nrows <= kTile) continue;           // this group's tile has no rows
       const int r = q * kTile + rl;                       // row of the unit
       const bool live = r < e.nrows;
       const int R = e.row0 + (live ? r : 0);
-      const int t = R / a.G, hq = e.h * a.G + (R - t * a.G);
+      const int t = R / a.G;
+      float sl2q = a.scale_log2, vref = 1.f;
       if (e.nu > 0) {
         // Q row into the swizzled tile (rows without a token: zeros)
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (e.s.cu0 + t) * a.q_tok + hq * a.q_head);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (e.s.cu0 + t) * a.q_tok + (e.h * a.G + (R - t * a.G)) * a.q_head);
         uint8_t* dst = sQ + q * C::kTileBytes + rl * 128;
+        uint4 x[D / 8];
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 x = live ? src[c] : make_uint4(0, 0, 0, 0);
-          *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kPanelBytes + (((c & 7) ^ (rl & 7)) << 4)) = x;
-        }
+        for (int c = 0; c < D / 8; ++c) x[c] = live ? src[c] : make_uint4(0, 0, 0, 0);
+        if constexpr (kFp8 && !kFp16) sl2q *= row_to_fp16<D / 2>(&x[0].x);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c)
+          *reinterpret_cast<uint4*>(dst + (c >> 3) * C::kPanelBytes + (((c & 7) ^ (rl & 7)) << 4)) = x[c];
         fence_async_smem();
         tc_fence_before();
         mbar_arrive(&sh.q_full[q]);
@@ -426,13 +675,21 @@ __global__ void __launch_bounds__(512, 1)
               if (!((vis >> i) & 1u)) s[32 * h + i] = -INFINITY;
           }
         }
+        float sl2 = sl2q;
+        // never 0, which would make NaN of a masked score's -inf
+        if constexpr (kFp8) sl2 = fmaxf(sl2 * *reinterpret_cast<volatile float*>(&sh.kfac[(tile0 + u) & 7]), 0x1p-126f);
         const float mx2 = row_max128(s) * sl2;
         float alpha = 1.f;
         if (mx2 > m) {
           alpha = ex2(m - mx2);                           // 0 when m = -inf
           m = mx2;
         }
-        sh.alpha[q][rl] = alpha;
+        if constexpr (kFp8) {
+          sh.alpha[q][rl] = alpha * *reinterpret_cast<volatile float*>(&sh.vfac[(tile0 + u) & 7]);
+          vref = *reinterpret_cast<volatile float*>(&sh.vref[(tile0 + u) & 7]);
+        } else {
+          sh.alpha[q][rl] = alpha;
+        }
         mbar_arrive(&sh.alpha_full[q]);
         const float mneg = (m == -INFINITY) ? 0.f : -m;
         const float2 sl2v = make_float2(sl2, sl2), mnegv = make_float2(mneg, mneg);
@@ -445,7 +702,7 @@ __global__ void __launch_bounds__(512, 1)
             const float2 x = fma2(make_float2(s[32 * h + 2 * i], s[32 * h + 2 * i + 1]), sl2v, mnegv);
             const float2 p = (((16 * h + i) & 7) < C::kPolyOf8) ? exp2_poly2(x) : make_float2(ex2(x.x), ex2(x.y));
             acc[i & 3] = add2(acc[i & 3], p);
-            pk[i] = pack2<kFp16>(p.x, p.y);               // at most half a 16-bit step; the sum keeps 32 bits
+            pk[i] = pack2<kMmaFp16>(p.x, p.y);            // at most half a 16-bit step; the sum keeps 32 bits
           }
           tmem_st16(tS + 16 * h, pk);
         }
@@ -468,8 +725,9 @@ __global__ void __launch_bounds__(512, 1)
       const int slot = 2 * blockIdx.x + (e.from_start ? 1 : 0);
       if (q == 0 && rl == 0 && e.from_start && !e.to_end)
         a.meta[blockIdx.x] = make_int4(e.b, e.unit, owner_cta(total, e.g + e.s.KT - 1, gridDim.x), 0);
-      const bool odd = e.nu > 0 && *reinterpret_cast<volatile int*>(&sh.odd[q][(nseg - 1) & 1]) == nseg;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const bool odd = e.nu > 0 && *reinterpret_cast<volatile int*>(&sh.odd[q][(nseg - 1) & 7]) == nseg;
+      const float inv = whole ? (l == 0.f ? 0.f : vref / l) : vref;
+      const int hq = e.h * a.G + (R - t * a.G);
       const long long tk = e.s.cu0 + t;
       if (live) {
         if (whole) {
@@ -496,12 +754,15 @@ __global__ void __launch_bounds__(512, 1)
             if (!(visible32(a, e.s, t, j) & 1u)) continue;
             const long long row = slot_row(a.c, e.b, e.h, (long long)e.s.len + j);
             if (row < 0) continue;
-            const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v) + row * D + cc;
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              constexpr uint32_t ex = kFp16 ? 0x7C00u : 0x7F80u;
-              const uint32_t w = v[i];
-              if ((w & ex) == ex) o[i] = __float_as_uint(__uint_as_float(o[i]) + unpack2<kFp16>(w).x);
+              if constexpr (kFp8) {
+                if ((a.c.v[row * D + cc + i] & 0x7F) == 0x7F) o[i] = 0x7FFFFFFFu;
+              } else {
+                constexpr uint32_t ex = kFp16 ? 0x7C00u : 0x7F80u;
+                const uint32_t x = reinterpret_cast<const uint16_t*>(a.c.v)[row * D + cc + i];
+                if ((x & ex) == ex) o[i] = __float_as_uint(__uint_as_float(o[i]) + unpack2<kFp16>(x).x);
+              }
             }
           }
         }
@@ -519,7 +780,13 @@ __global__ void __launch_bounds__(512, 1)
         } else {
           uint4* dst = reinterpret_cast<uint4*>(a.part_o + ((long long)slot * a.slot_rows + r) * D + cc);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          for (int i = 0; i < 8; ++i) {
+            if constexpr (kFp8) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[4 * i + k] = __float_as_uint(__uint_as_float(o[4 * i + k]) * inv);
+            }
+            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
         }
       }
       tc_fence_before();                                  // O is read: the next segment may overwrite it
@@ -534,10 +801,10 @@ __global__ void __launch_bounds__(512, 1)
   }
 }
 
-template <int D, bool kFp16>
+template <int D, bool kFp8, bool kFp16>
 cudaError_t launch_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, cudaStream_t s) {
-  using C = BigCfg<D>;
-  auto kern = tree_big_kernel<D, kFp16>;
+  using C = BigCfg<D, kFp8>;
+  auto kern = tree_big_kernel<D, kFp8, kFp16>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (e != cudaSuccess) return e;
   // setmaxnreg.inc waits until the block's launch registers cover every warpgroup's share: refuse a
@@ -554,12 +821,18 @@ cudaError_t launch_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeA
   return cudaGetLastError();
 }
 
+template <int D>
+cudaError_t launch_big_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp8, bool fp16, int ctas,
+                         cudaStream_t s) {
+  if (fp8) return fp16 ? launch_big<D, true, true>(tk, tv, a, ctas, s) : launch_big<D, true, false>(tk, tv, a, ctas, s);
+  return fp16 ? launch_big<D, false, true>(tk, tv, a, ctas, s) : launch_big<D, false, false>(tk, tv, a, ctas, s);
+}
+
 }  // namespace
 
-cudaError_t launch_tree_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp16, int ctas,
-                            cudaStream_t s) {
-  if (a.c.d == 128) return fp16 ? launch_big<128, true>(tk, tv, a, ctas, s) : launch_big<128, false>(tk, tv, a, ctas, s);
-  return fp16 ? launch_big<64, true>(tk, tv, a, ctas, s) : launch_big<64, false>(tk, tv, a, ctas, s);
+cudaError_t launch_tree_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp8, bool fp16,
+                            int ctas, cudaStream_t s) {
+  return a.c.d == 128 ? launch_big_d<128>(tk, tv, a, fp8, fp16, ctas, s) : launch_big_d<64>(tk, tv, a, fp8, fp16, ctas, s);
 }
 
 }  // namespace fa

@@ -493,7 +493,7 @@ int fa_cache_keep(const fa_cache_keep_args* args);
  *               their own
  * A row that sees no key gets O = 0 and LSE = -inf.  Keys and values that a row does not see do
  * not enter its result, whatever they hold.  Tokens outside cu_new[0] .. cu_new[B] - 1 are left as
- * they are in o and lse.  An E4M3 cache's values must be finite in dtype.  At most two launches.
+ * they are in o and lse.  At most two launches.
  */
 typedef struct {
   fa_cache cache;

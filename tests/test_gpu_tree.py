@@ -109,30 +109,67 @@ def test_values_a_row_does_not_see_do_not_reach_it(G, n, dtype, fp8):
     check_attention(c, q, o, lse, 1 / 8, bits, nan_ok=True)
 
 
+@pytest.mark.parametrize("n", [2, 40])
 @pytest.mark.parametrize("dtype", [BF, HF])
-def test_nan_codes_of_the_prefix(dtype):
+def test_nan_codes_of_the_prefix(dtype, n):
     """A NaN in the prefix reaches every row's result (V: its column) and nothing hides it."""
-    c = Case([200], [2], 2, 64, 16, dtype, True, seed=5)
+    c = Case([200], [n], 2, 64, 16, dtype, True, seed=5)
     c.put(c.new(2), c.new(2))
     p, r = c.table_np[0, 3], 5
     c.gpu["v"][p, 0, r, 17] = 127
     c.gpu["k"][p, 1, r, 9] = 255
     q = c.new(4).cuda()
-    o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, 2)
+    o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, n)
     fa.fa_check_status()
     check_attention(c, q, o, lse, 1 / 8, nan_ok=True)
     assert torch.isnan(o[:, :2, 17]).all() and torch.isnan(o[:, 2:]).all()
 
 
+@pytest.mark.parametrize("n", [1, 40])
 @pytest.mark.parametrize("fp8", [False, True])
-def test_long_peaked_rows(fp8):
-    """Scores in the tens, growing along the keys: the running max changes all the way."""
-    c = Case([4000], [1], 1, 128, 64, BF, fp8, seed=9, k_gain=4.0 if not fp8 else 1.0)
+def test_long_peaked_rows(fp8, n):
+    """Scores in the tens: the running max changes all the way."""
+    c = Case([2000], [n], 1, 128, 64, BF, fp8, seed=9, k_gain=4.0 if not fp8 else 1.0)
     c.put(c.new(1), c.new(1))
     q = (c.new(4) * 4).cuda()
-    o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, 1)
+    o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, n)
     fa.fa_check_status()
     check_attention(c, q, o, lse, 1 / 128 ** 0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("n", [1, 48])
+def test_scales_that_differ_widely_along_the_keys(dtype, n):
+    """K and V rows whose magnitudes rise by steps of up to 2^12 along the keys and fall again, and rows
+    of zeros: every rescale of the E4M3 path."""
+    c = Case([700], [n], 1, 64, 16, dtype, True, seed=6)
+    c.put(c.new(1), c.new(1))
+    for p in range(700):
+        i, r = c.table_np[0, p // 16], p % 16
+        up = (0, 3, 9, 12, 24, 13, -6)[p // 100]
+        c.gpu["v_scale"][i, :, r] = 112 + up - (5 if p % 3 else 0)
+        c.gpu["k_scale"][i, :, r] = 118 - (6 if p % 5 else 0) + (2 if p > 500 else 0)
+        if p % 50 == 0:
+            c.gpu["v"][i, :, r] = 0
+            c.gpu["v_scale"][i, :, r] = 1
+    q = c.new(2).cuda()
+    o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, n)
+    fa.fa_check_status()
+    check_attention(c, q, o, lse, 1 / 8)
+
+
+def test_bf16_queries_of_any_size_over_codes():
+    """Rows of Q far outside fp16's range (their products are made in fp16)."""
+    for n in (2, 40):
+        c = Case([300], [n], 1, 64, 16, BF, True, seed=8)
+        c.gpu["k_scale"].fill_(60)
+        c.put((c.new(1).float() * 2.0 ** -60).to(BF), c.new(1))
+        q = (c.new(1).float() * 2.0 ** 60).to(BF)
+        q[1] = 0
+        q = q.cuda()
+        o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, n)
+        fa.fa_check_status()
+        check_attention(c, q, o, lse, 1 / 8)
 
 
 def test_lengths_on_the_device_are_what_a_replayed_graph_reads():
