@@ -27,6 +27,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 __all__ = [
     "FAError", "fa_fwd", "fa_bwd", "fa_fwd_ex", "fa_bwd_ex", "fa_bwd_workspace_bytes",
@@ -53,6 +54,7 @@ _vp = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _ll = ctypes.c_longlong
+_bytes = ctypes.c_char_p
 
 
 class FwdArgs(ctypes.Structure):
@@ -179,13 +181,13 @@ def lib() -> ctypes.CDLL:
     L.fa_selftest_wait_timeout.restype = _i
     L.fa_selftest_exp2_poly.argtypes = [_vp, _vp, _i, _vp]
     L.fa_selftest_exp2_poly.restype = _i
-    L.fa_cache_append.argtypes = [ctypes.POINTER(CacheAppendArgs)]
+    L.fa_cache_append.argtypes = [_bytes]                # the bytes of a CacheAppendArgs
     L.fa_cache_append.restype = _i
-    L.fa_cache_read.argtypes = [ctypes.POINTER(CacheReadArgs)]
+    L.fa_cache_read.argtypes = [_bytes]                # the bytes of a CacheReadArgs
     L.fa_cache_read.restype = _i
-    L.fa_cache_keep.argtypes = [ctypes.POINTER(CacheKeepArgs)]
+    L.fa_cache_keep.argtypes = [_bytes]                # the bytes of a CacheKeepArgs
     L.fa_cache_keep.restype = _i
-    L.fa_fwd_tree.argtypes = [ctypes.POINTER(TreeArgs)]
+    L.fa_fwd_tree.argtypes = [_bytes]                    # the bytes of a TreeArgs
     L.fa_fwd_tree.restype = _i
     L.fa_fwd_tree_workspace_bytes.argtypes = [_i, _i, _i, _i]
     L.fa_fwd_tree_workspace_bytes.restype = ctypes.c_size_t
@@ -329,21 +331,32 @@ def fa_fwd_fp8(q8, k8, v8, descale_q, descale_k, descale_v, o, lse, B, H, N, d, 
     _check(lib().fa_fwd_fp8(ctypes.byref(a)), "fa_fwd_fp8")
 
 
+# The serving calls are made once per layer and token, so their argument blocks are packed as bytes
+# (the structs' native layout, the cache's block first) instead of through ctypes fields.
+_pack_append = struct.Struct("@PPqqqqPPiiP").pack
+_pack_read = struct.Struct("@PPPiiP").pack
+_pack_keep = struct.Struct("@PPPiP").pack
+_pack_tree = struct.Struct("@PPPqqqqPPPiiiiifPNP").pack
+
+
 def fa_cache_append(cache, k_new, v_new, k_strides, v_strides, cu_new, lens, total, dtype, stream=None):
-    """cache: a CacheArgs; strides: (token, head) in elements."""
-    a = CacheAppendArgs(cache, _ptr(k_new), _ptr(v_new), *k_strides, *v_strides, _ptr(cu_new), _ptr(lens), total,
-                        dtype, _stream(stream))
-    _check(lib().fa_cache_append(ctypes.byref(a)), "fa_cache_append")
+    """cache: the bytes of a CacheArgs; strides: (token, head) in elements."""
+    rc = lib().fa_cache_append(cache + _pack_append(_ptr(k_new), _ptr(v_new), *k_strides, *v_strides, _ptr(cu_new),
+                                                    _ptr(lens), total, dtype, _stream(stream)))
+    if rc:
+        raise FAError(rc, "fa_cache_append")
 
 
 def fa_cache_read(cache, lens, k_out, v_out, N, dtype, stream=None):
-    a = CacheReadArgs(cache, _ptr(lens), _ptr(k_out), _ptr(v_out), N, dtype, _stream(stream))
-    _check(lib().fa_cache_read(ctypes.byref(a)), "fa_cache_read")
+    rc = lib().fa_cache_read(cache + _pack_read(_ptr(lens), _ptr(k_out), _ptr(v_out), N, dtype, _stream(stream)))
+    if rc:
+        raise FAError(rc, "fa_cache_read")
 
 
 def fa_cache_keep(cache, lens, kept, counts, width, stream=None):
-    a = CacheKeepArgs(cache, _ptr(lens), _ptr(kept), _ptr(counts), width, _stream(stream))
-    _check(lib().fa_cache_keep(ctypes.byref(a)), "fa_cache_keep")
+    rc = lib().fa_cache_keep(cache + _pack_keep(_ptr(lens), _ptr(kept), _ptr(counts), width, _stream(stream)))
+    if rc:
+        raise FAError(rc, "fa_cache_keep")
 
 
 def fa_fwd_tree_workspace_bytes(total: int, Hq: int, Hk: int, d: int) -> int:
@@ -352,11 +365,12 @@ def fa_fwd_tree_workspace_bytes(total: int, Hq: int, Hk: int, d: int) -> int:
 
 def fa_fwd_tree(cache, q, o, lse, q_strides, o_strides, cu_new, lens, tree_mask, mask_words, total, Hq, max_new,
                 dtype, scale, workspace, workspace_bytes, stream=None):
-    """cache: a CacheArgs; strides: (token, head) in elements."""
-    a = TreeArgs(cache, _ptr(q), _ptr(o), _ptr(lse), *q_strides, *o_strides, _ptr(cu_new), _ptr(lens),
-                 _ptr(tree_mask), mask_words, total, Hq, max_new, dtype, scale, _ptr(workspace), workspace_bytes,
-                 _stream(stream))
-    _check(lib().fa_fwd_tree(ctypes.byref(a)), "fa_fwd_tree")
+    """cache: the bytes of a CacheArgs; strides: (token, head) in elements."""
+    rc = lib().fa_fwd_tree(cache + _pack_tree(_ptr(q), _ptr(o), _ptr(lse), *q_strides, *o_strides, _ptr(cu_new),
+                                              _ptr(lens), _ptr(tree_mask) or 0, mask_words, total, Hq, max_new,
+                                              dtype, scale, _ptr(workspace), workspace_bytes, _stream(stream)))
+    if rc:
+        raise FAError(rc, "fa_fwd_tree")
 
 
 def _event(e):
@@ -383,9 +397,9 @@ def fa_bwd_ex(q, k, v, o, lse, dout, dq, dk, dv, B, H, N, d, scale, causal=False
 
 def _dtype_code(t):
     import torch
-    if t.dtype == torch.bfloat16:
+    if t.dtype is torch.bfloat16:
         return FA_BF16
-    if t.dtype == torch.float16:
+    if t.dtype is torch.float16:
         return FA_FP16
     raise TypeError(f"unsupported dtype {t.dtype}")
 
@@ -536,27 +550,32 @@ class KVCache:
             raise ValueError("expected page_table as an int32 CUDA tensor [B, max_pages]")
         self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
         self.device = k.device
+        self.index = k.get_device()
         for t in (v, k_scale, v_scale, page_table):
             if t is not None and t.device != k.device:
                 raise ValueError("the cache's tensors are on different devices")
         self.pages, self.Hk, self.page_size, self.d = k.shape
         self.B, self.max_pages = page_table.shape
-        self.args = CacheArgs(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), self.pages, self.Hk,
-                              self.page_size, self.d, self.dtype, self.B, self.max_pages,
-                              page_table.stride(0) if self.B > 1 else max(self.max_pages, 1))
+        args = CacheArgs(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), self.pages, self.Hk,
+                         self.page_size, self.d, self.dtype, self.B, self.max_pages,
+                         page_table.stride(0) if self.B > 1 else max(self.max_pages, 1))
+        self.args = bytes(args)
+        self._per_sequence, self._bounds = (self.B,), (self.B + 1,)
 
-    def _lengths(self, *named):
+    def _lengths(self, name, t, shape):
         import torch
-        for name, t, n in named:
-            if not (t.device == self.device and t.dtype == torch.int32 and t.is_contiguous() and t.shape == n):
-                raise ValueError(f"expected {name} as a contiguous int32 tensor {list(n)} on the cache's device")
+        if not (t.get_device() == self.index and t.dtype is torch.int32 and t.shape == shape and t.is_contiguous()):
+            raise ValueError(f"expected {name} as a contiguous int32 tensor {list(shape)} on the cache's device")
 
     def _rows(self, name, t, heads):
         """(token, head) strides of a [total, heads, d] tensor; heads None: any multiple of Hk."""
-        if not (t.device == self.device and t.dim() == 3 and t.shape[2] == self.d and t.stride(2) == 1
-                and (t.shape[1] == heads if heads is not None else t.shape[1] > 0 and t.shape[1] % self.Hk == 0)):
-            raise ValueError(f"expected {name} as [total, heads, {self.d}] on the cache's device, its last dimension contiguous")
-        return (t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0)
+        shape = t.shape
+        if (t.get_device() == self.index and len(shape) == 3 and shape[2] == self.d
+                and (shape[1] == heads if heads is not None else shape[1] > 0 and shape[1] % self.Hk == 0)):
+            st, sh, sd = t.stride()
+            if sd == 1:
+                return st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
+        raise ValueError(f"expected {name} as [total, heads, {self.d}] on the cache's device, its last dimension contiguous")
 
     def _type(self, t):
         code = _dtype_code(t)
@@ -565,13 +584,16 @@ class KVCache:
         return code
 
 
-def _on_device(cache, call, *args):
-    """Run ``call`` with the cache's device current (CUDA launches go to the current device)."""
+def _on_device(cache, call, *args, stream=None):
+    """Run ``call`` on ``stream``, or the current stream of the cache's device, with that device
+    current (CUDA launches go to the current device)."""
     import torch
-    if cache.device.index == torch.cuda.current_device():
-        return call(*args)
-    with torch.cuda.device(cache.device):
-        return call(*args)
+    if stream is None:
+        stream = torch._C._cuda_getCurrentRawStream(cache.index)
+    if cache.index == torch._C._cuda_getDevice():
+        return call(*args, stream)
+    with torch.cuda.device(cache.index):
+        return call(*args, stream)
 
 
 def cache_append(cache, k_new, v_new, cu_new, lens, stream=None):
@@ -579,11 +601,12 @@ def cache_append(cache, k_new, v_new, cu_new, lens, stream=None):
     will do), behind what each sequence holds (fa_cache_append): token cu_new[b] + i goes to position
     lens[b] + i of sequence b.  ``lens`` is not changed.  An E4M3 cache quantises them."""
     ks, vs = cache._rows("k_new", k_new, cache.Hk), cache._rows("v_new", v_new, cache.Hk)
-    if v_new.shape != k_new.shape or v_new.dtype != k_new.dtype:
+    if v_new.shape[0] != k_new.shape[0] or v_new.dtype is not k_new.dtype:
         raise ValueError("k_new and v_new differ in shape or type")
-    cache._lengths(("cu_new", cu_new, (cache.B + 1,)), ("lens", lens, (cache.B,)))
+    cache._lengths("cu_new", cu_new, cache._bounds)
+    cache._lengths("lens", lens, cache._per_sequence)
     _on_device(cache, fa_cache_append, cache.args, k_new, v_new, ks, vs, cu_new, lens, k_new.shape[0],
-               cache._type(k_new), stream)
+               cache._type(k_new), stream=stream)
 
 
 def cache_read(cache, lens, N, dtype=None, k_out=None, v_out=None, stream=None):
@@ -591,7 +614,7 @@ def cache_read(cache, lens, N, dtype=None, k_out=None, v_out=None, stream=None):
     (fa_cache_read).  ``dtype``: of an E4M3 cache's result, torch.bfloat16 (default) or float16;
     ``k_out``, ``v_out``: tensors to write to."""
     import torch
-    cache._lengths(("lens", lens, (cache.B,)))
+    cache._lengths("lens", lens, cache._per_sequence)
     shape = (cache.B, cache.Hk, N, cache.d)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else torch.bfloat16 if cache.dtype == FA_E4M3 else cache.k.dtype
@@ -600,9 +623,9 @@ def cache_read(cache, lens, N, dtype=None, k_out=None, v_out=None, stream=None):
     if v_out is None:
         v_out = torch.empty(shape, dtype=dtype, device=cache.device)
     for t in (k_out, v_out):
-        if not (t.device == cache.device and t.shape == shape and t.is_contiguous() and t.dtype == dtype):
+        if not (t.get_device() == cache.index and t.shape == shape and t.is_contiguous() and t.dtype is dtype):
             raise ValueError(f"expected k_out and v_out as contiguous {dtype} tensors {list(shape)}")
-    _on_device(cache, fa_cache_read, cache.args, lens, k_out, v_out, N, cache._type(k_out), stream)
+    _on_device(cache, fa_cache_read, cache.args, lens, k_out, v_out, N, cache._type(k_out), stream=stream)
     return k_out, v_out
 
 
@@ -612,8 +635,11 @@ def cache_keep(cache, lens, kept, counts, stream=None):
     int32 [B].  ``lens`` is not changed."""
     if kept.dim() != 2:
         raise ValueError("expected kept as [B, width]")
-    cache._lengths(("lens", lens, (cache.B,)), ("kept", kept, (cache.B, kept.shape[1])), ("counts", counts, (cache.B,)))
-    _on_device(cache, fa_cache_keep, cache.args, lens, kept, counts, kept.shape[1], stream)
+    width = kept.shape[1]
+    cache._lengths("lens", lens, cache._per_sequence)
+    cache._lengths("kept", kept, (cache.B, width))
+    cache._lengths("counts", counts, cache._per_sequence)
+    _on_device(cache, fa_cache_keep, cache.args, lens, kept, counts, width, stream=stream)
 
 
 def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scale=None, workspace=None, o=None,
@@ -627,30 +653,31 @@ def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scal
     qs = cache._rows("q", q, None)
     code = cache._type(q)
     total, Hq, d = q.shape
-    cache._lengths(("cu_new", cu_new, (cache.B + 1,)), ("lens", lens, (cache.B,)))
+    cache._lengths("cu_new", cu_new, cache._bounds)
+    cache._lengths("lens", lens, cache._per_sequence)
     words = 0
     if tree_mask is not None:
-        if not (tree_mask.device == cache.device and tree_mask.dtype == torch.int64 and tree_mask.dim() == 2
+        if not (tree_mask.get_device() == cache.index and tree_mask.dtype is torch.int64 and tree_mask.dim() == 2
                 and tree_mask.is_contiguous() and tree_mask.shape[0] == total):
             raise ValueError("expected tree_mask as a contiguous int64 tensor [total, words] on the cache's device")
         words = tree_mask.shape[1]
     if o is None:
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif o.shape != q.shape or o.dtype != q.dtype:
+    elif o.shape[0] != total or o.dtype is not q.dtype:
         raise ValueError("o and q differ in shape or type")
     os_ = cache._rows("o", o, Hq)
     if lse is None:
         lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
-    elif not (lse.device == cache.device and lse.dtype == torch.float32 and lse.shape == (total, Hq)
+    elif not (lse.get_device() == cache.index and lse.dtype is torch.float32 and lse.shape == (total, Hq)
               and lse.is_contiguous()):
         raise ValueError("expected lse as a contiguous float32 tensor [total, Hq]")
     if workspace is None:
         workspace = torch.empty(fa_fwd_tree_workspace_bytes(total, Hq, cache.Hk, d), dtype=torch.uint8, device=q.device)
-    elif not (workspace.device == cache.device and workspace.is_contiguous()):
+    elif not (workspace.get_device() == cache.index and workspace.is_contiguous()):
         raise ValueError("expected workspace as a contiguous tensor on the cache's device")
     _on_device(cache, fa_fwd_tree, cache.args, q, o, lse, qs, os_, cu_new, lens, tree_mask, words, total, Hq,
                int(max_new), code, 1.0 / d ** 0.5 if scale is None else scale, workspace,
-               workspace.numel() * workspace.element_size(), stream)
+               workspace.numel() * workspace.element_size(), stream=stream)
     return o, lse
 
 

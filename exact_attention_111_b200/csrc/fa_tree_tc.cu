@@ -4,10 +4,11 @@
 // A unit's row tile is 256 rows (two 128-row MMA tiles that share every K/V tile); CTA c walks its part
 // of the line of chunks (fa_cache.cuh), one chunk = one 128-key tile.  Warp roles (512 threads):
 //   warps 0-3, 4-7  softmax groups 0, 1: Q rows into shared memory, then one row per thread
-//   warps 8-11      correction: O_q <- alpha O_q in TMEM; makes the V tiles that hold new tokens safe
-//   warp  12        producer: the K/V ring by TMA, one box per page and 128-byte panel
+//   warps 8-11      correction: O_q <- alpha O_q in TMEM; makes the V tiles that hold new tokens safe;
+//                   E4M3: expands V into the ring
+//   warp  12        producer: the K/V ring by TMA, one box per page and 128-byte panel (E4M3: the codes)
 //   warp  13        MMA issuer (one thread) and TMEM allocator
-//   warps 14-15     complete the producer's warpgroup
+//   warps 14-15     E4M3: expand K into the ring
 // Tensor memory (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+d), O1 [256+d,256+2d); P
 // (16-bit) over the first 64 columns of its S.  Per tile u: O_q += P_q V(u-1), then S_q = Q_q K(u)^T, so
 // a finished S_q(u) also says that O_q holds every earlier product.
@@ -97,10 +98,10 @@ struct BigShared {
   // writes them is at most kStages + 1 tiles, so 5 segments, ahead of the slower softmax group.
   int odd[2][8];
   float alpha[2][kTile];
-  // E4M3: staged scale codes of a tile, and by tile mod 8 the factors of its K, of what O holds and
-  // of O (see the converter).  Entry u is written again for tile u + 8, whose K slot is free only
+  // E4M3: staged scale codes of a tile (K's and V's with K, V's with V), and by tile mod 8 the factors of its K, of what O
+  // holds and of O.  Entry u is written again for tile u + 8, whose K slot is free only
   // after S of tile u + 8 - kStages, so of u + 4, which waited for both softmax groups to have finished u + 3.
-  alignas(16) uint8_t scales[2][kTile];
+  alignas(16) uint8_t scales[3][kTile];
   float kfac[8], vfac[8], vref[8];
   Walk walk[8];                  // one per softmax warp, whose registers are full
 };
@@ -143,182 +144,193 @@ __device__ __forceinline__ uint32_t visible32(const TreeArgs& a, const SeqView& 
 // tiles' scales are at most 2^7 larger (448 * 2^7 is the last that fp16 holds); one that is larger
 // becomes E, and what O holds is scaled down with the softmax's own rescale.
 //
-// Three warps (12, 14, 15; 96 threads).  Warp 12 keeps one tile's codes of K and of V ahead in shared
-// memory by TMA, all three expand them into the ring's tiles.  In tiles that hold new tokens V's rows
-// past the end become zero and so do NaN codes, noted (see the top of the file).
-template <int D, bool kFp8, bool kFp16>
-__device__ void convert_role(const TreeArgs& a, BigShared& sh, uint8_t* sK, uint8_t* sV, uint8_t* sC,
-                             const CUtensorMap* tm_k, const CUtensorMap* tm_v, Walk& w, const Cursor& cur,
-                             const Part& part) {
-  using C = BigCfg<D, kFp8>;
-  constexpr int kLanes = D / 16;                          // 16-code chunks of a row
+// Warp 12 keeps one tile's codes of K and of V ahead in shared memory by TMA.  Warps 14 and 15 expand
+// K into the ring; the correction warps expand V, one tile ahead of their rescales.  In tiles that hold
+// new tokens V's rows past the end become zero and so do NaN codes, noted (see the top of the file).
+
+// fp16 2^d twice, d <= 15; 0 below the type's last bit.
+__device__ __forceinline__ uint32_t half2_pow2(int d) {
+  const uint32_t h = d >= -14 ? (uint32_t)(min(d, 15) + 15) << 10 : d >= -24 ? 1u << (d + 24) : 0u;
+  return h | (h << 16);
+}
+
+// The largest of a tile's first `keys` scale codes; one warp.
+__device__ __forceinline__ uint32_t top_scale(const uint8_t* scales, int keys) {
+  const int lane = lane_id(), k = keys - 4 * lane;
+  uint32_t x = *reinterpret_cast<const uint32_t*>(scales + 4 * lane);
+  x &= k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
+  return __reduce_max_sync(0xffffffffu, max(max(x & 0xFF, (x >> 8) & 0xFF), max((x >> 16) & 0xFF, x >> 24)));
+}
+
+// E of V after a tile whose largest scale is ev.
+__device__ __forceinline__ uint32_t next_eref(uint32_t eref, uint32_t ev, bool first) {
+  return first || ev > eref + 7 ? ev : eref;
+}
+
+// Expand one tile (128 rows of D codes, as TMA staged them) into a ring tile: warp wi of nW.  A pass
+// of a warp is 32 / kLanes rows; row factors are computed once, two or one per lane, and
+// shuffled.  clean (V): rows from `keys` on become zero and NaN codes too; returns whether there were.
+template <int D, int nW>
+__device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, const uint8_t* scales, int e, int wi,
+                                            bool clean, int keys) {
+  constexpr int kLanes = D / 16, kW = 32 / kLanes, kF = kTile / nW / 32, kPasses = kTile / (nW * kW);
   const int lane = lane_id();
-  const bool loader = warp_id() == C::kLoadWarp;
-  const int ci = loader ? lane : 32 + (warp_id() - C::kMmaWarp - 1) * 32 + lane;
+  const int chunk = lane % kLanes, sub = lane / kLanes;
+  uint32_t f[kF];
+#pragma unroll
+  for (int k = 0; k < kF; ++k) {
+    const int j = k * 32 + lane;
+    f[k] = half2_pow2((int)scales[(j / kW) * (nW * kW) + wi * kW + j % kW] - e);
+  }
+  bool odd = false;
+  // chunk `chunk` of the codes (16) is chunks 2 chunk, 2 chunk + 1 of the row (8 values each); at d =
+  // 128 half of the lanes start with the second, so that a quarter warp's stores hit all banks
+  const int r0 = wi * kW + sub;
+  const int c0 = (2 * chunk) & 7, sw = D == 128 ? (chunk >> 2) & 1 : 0;
+  uint8_t* dst = dst0 + (chunk >> 2) * (kTile * 128);
+  static_assert(kPasses % 4 == 0, "passes");
+#pragma unroll 1
+  for (int i0 = 0; i0 < kPasses; i0 += 4) {               // four passes' loads in flight
+    uint2 x[4][2];
+    uint32_t fi[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int p = i0 + i, r = r0 + p * nW * kW;
+      const uint8_t* src = src0 + (D == 64 ? r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4) : r * 128 + ((chunk ^ (r & 7)) << 4));
+      x[i][0] = *reinterpret_cast<const uint2*>(src + 8 * sw);
+      x[i][1] = *reinterpret_cast<const uint2*>(src + 8 - 8 * sw);
+      fi[i] = __shfl_sync(0xffffffffu, kF > 1 && p * kW >= 32 ? f[kF - 1] : f[0], (p * kW) % 32 + sub);
+    }
+    if (clean) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool past = r0 + (i0 + i) * nW * kW >= keys;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t& y = (k & 1) ? x[i][k >> 1].y : x[i][k >> 1].x;
+          if (past) y = 0;
+          const uint32_t b = ((y & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;   // NaN: 0x7F + 1 carries into bit 7
+          if (b != 0) {
+            y &= ~((b >> 7) * 0xFFu);
+            odd = true;
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = r0 + (i0 + i) * nW * kW;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t o[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t y = j < 2 ? x[i][k].x : x[i][k].y;
+          const uint32_t h = e4m3_to_f16x2((j & 1) ? y >> 16 : y);
+          const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&fi[i]));
+          o[j] = *reinterpret_cast<const uint32_t*>(&v);
+        }
+        *reinterpret_cast<uint4*>(dst + r * 128 + (((c0 + (k ^ sw)) ^ (r & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+      }
+    }
+  }
+  return odd;
+}
+
+__device__ __forceinline__ void l2_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z) : "memory");
+}
+
+// Warp 12 with an E4M3 cache: K's codes with both sets of scale codes, V's codes with V's.
+template <int D>
+__device__ void stage_role(const TreeArgs& a, BigShared& sh, uint8_t* sC, const CUtensorMap* tm_k,
+                           const CUtensorMap* tm_v, Walk& w) {
+  constexpr int kCodes = kTile * D;
+  const int lane = lane_id();
   const DevStatus st{a.c.status, a.timeout_ns};
   volatile int* abort_flag = &sh.abort_flag;
   const int R = 1 << a.c.page_shift, boxes = kTile / R;
-  const int chunk = ci % kLanes, row0 = ci / kLanes;
   const Seg& e = w.e;
-
-  // ---- staging (warp 12): tile nl's codes, K's with both sets of scale codes
-  Walk lw;
-  int lu = 0, nl[2] = {0, 0};
-  bool more = false, ok = true;
-  if (loader) {
-    lw.start(cur, part);
-    do more = lw.next(a); while (more && lw.e.nu == 0);
-    if (lane == 0) {
-      prefetch_tmap(tm_k);
-      prefetch_tmap(tm_v);
-    }
+  int n[2] = {0, 0};
+  bool ok = true;
+  if (lane == 0) {
+    prefetch_tmap(tm_k);
+    prefetch_tmap(tm_v);
   }
-  auto stage = [&](int which) {                           // K (0) then V (1) of the loader's tile
-    if (!loader || !more || !ok) return;
-    if (nl[which] > 0) ok = mbar_wait(&sh.c_empty[which], (nl[which] - 1) & 1, abort_flag, st);
-    if (!__all_sync(0xffffffffu, ok)) { ok = false; return; }
-    const int pos = (lw.e.kt0 + lu) * kChunk + lane * R;
-    int row = (int)((long long)a.c.pages * a.c.Hk << a.c.page_shift);   // behind the last row: zeros
-    bool valid = false;
-    if (lane < boxes && pos < lw.e.s.len + lw.e.s.T) {
-      const long long r = slot_row(a.c, lw.e.b, lw.e.h, pos);
-      if (r >= 0) {
-        row = (int)r;
-        valid = true;
-      }
-    }
-    const int nvalid = __popc(__ballot_sync(0xffffffffu, valid));
-    if (lane == 0) mbar_arrive_expect_tx(&sh.c_full[which], C::kCodes + (which == 0 ? 2 * nvalid * R : 0));
-    __syncwarp();
-    if (lane < boxes) {
-      tma_load_3d(sC + which * C::kCodes + lane * R * D, which == 0 ? tm_k : tm_v, &sh.c_full[which], 0, row, 0);
-      if (which == 0 && valid) {
-        bulk_load(&sh.scales[0][lane * R], a.c.ks + row, R, &sh.c_full[0]);
-        bulk_load(&sh.scales[1][lane * R], a.c.vs + row, R, &sh.c_full[0]);
-      }
-    }
-    ++nl[which];
-    if (which == 1 && ++lu >= lw.e.nu) {
-      lu = 0;
-      do more = lw.next(a); while (more && lw.e.nu == 0);
-    }
-    __syncwarp();
-  };
-  stage(0);
-  stage(1);
-
-  int n = 0;                                              // tiles converted
-  int seg[2] = {0, 0};
-  uint32_t eref = 0;
   while (ok && w.next(a)) {
-    const int nq = e.nrows > kTile ? 2 : 1;
-    for (int u = 0; u < e.nu && ok; ++u, ++n) {
-      const int kt = e.kt0 + u;
-      const int keys = min(kTile, e.s.len + e.s.T - kt * kChunk);
-      const bool tail = tail_tile(e, kt);
-      const int s = n % C::kStages;
-      const uint32_t ph = ((n / C::kStages) - 1) & 1;
-      uint32_t sv[(kTile * kLanes + 95) / 96 / 4 + 1];    // V scale codes of this thread's rows
-      uint32_t ek = 0;
-#pragma unroll
-      for (int which = 0; which < 2; ++which) {
-        ok = mbar_wait(&sh.c_full[which], n & 1, abort_flag, st);
-        if (ok && n >= C::kStages) ok = mbar_wait(which == 0 ? &sh.k_empty[s] : &sh.v_empty[s], ph, abort_flag, st);
-        if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-        if (which == 0) {
-          // the largest scale codes of K and V among the keys that exist
-          uint32_t x = *reinterpret_cast<const uint32_t*>(&sh.scales[0][4 * lane]);
-          uint32_t y = *reinterpret_cast<const uint32_t*>(&sh.scales[1][4 * lane]);
-          const int k = keys - 4 * lane;
-          const uint32_t keep = k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
-          x &= keep;
-          y &= keep;
-          x = max(max(x & 0xFF, (x >> 8) & 0xFF), max((x >> 16) & 0xFF, x >> 24));
-          y = max(max(y & 0xFF, (y >> 8) & 0xFF), max((y >> 16) & 0xFF, y >> 24));
-          ek = __reduce_max_sync(0xffffffffu, x);
-          const uint32_t ev = __reduce_max_sync(0xffffffffu, y);
-          float vfac = 1.f;
-          if (u == 0) {
-            eref = ev;
-          } else if (ev > eref + 7) {
-            vfac = exp2f((float)eref - (float)ev);
-            eref = ev;
-          }
-          if (ci == 0) {
-            *reinterpret_cast<volatile float*>(&sh.kfac[n & 7]) = scale_value(ek);
-            *reinterpret_cast<volatile float*>(&sh.vfac[n & 7]) = vfac;
-            *reinterpret_cast<volatile float*>(&sh.vref[n & 7]) = scale_value(eref);
-          }
+    for (int u = 0; u < e.nu && ok; ++u) {
+      const int pos = (e.kt0 + u) * kChunk + lane * R;
+      int row = (int)((long long)a.c.pages * a.c.Hk << a.c.page_shift);   // behind the last row: zeros
+      bool valid = false;
+      if (lane < boxes && pos < e.s.len + e.s.T) {
+        const long long r = slot_row(a.c, e.b, e.h, pos);
+        if (r >= 0) {
+          row = (int)r;
+          valid = true;
         }
-        uint8_t* dst0 = (which == 0 ? sK : sV) + s * C::kTileBytes;
-        const uint8_t* src0 = sC + which * C::kCodes;
-        bool odd = false;
+      }
+      const int nvalid = __popc(__ballot_sync(0xffffffffu, valid));
+      if (valid) {                                        // one buffer each: have the copies start from L2
+        l2_prefetch_3d(tm_k, 0, row, 0);
+        l2_prefetch_3d(tm_v, 0, row, 0);
+      }
 #pragma unroll
-        for (int i = 0; i < (kTile * kLanes + 95) / 96; ++i) {
-          const int r = row0 + i * (96 / kLanes);
-          if (r < kTile) {
-            uint4 x = *reinterpret_cast<const uint4*>(
-                src0 + (D == 64 ? r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4) : r * 128 + ((chunk ^ (r & 7)) << 4)));
-            // V's scale codes are staged with K's: keep this thread's before K's staging is released
-            uint32_t code;
-            if (which == 0) {
-              code = sh.scales[0][r];
-              if ((i & 3) == 0) sv[i >> 2] = 0;
-              sv[i >> 2] |= (uint32_t)sh.scales[1][r] << (8 * (i & 3));
-            } else {
-              code = (sv[i >> 2] >> (8 * (i & 3))) & 0xFF;
-              if (tail) {
-                if (r >= keys) {
-                  x = make_uint4(0, 0, 0, 0);
-                  code = 0;
-                }
-                uint32_t* y = &x.x;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {             // NaN codes: 0x7F + 1 carries into bit 7
-                  const uint32_t b = ((y[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
-                  if (b != 0) {
-                    y[j] &= ~((b >> 7) * 0xFFu);
-                    odd = true;
-                  }
-                }
-              }
-            }
-            const int d = max((int)code - (int)(which == 0 ? ek : eref), -24);
-            const uint32_t f1 = pack2<true>(scale_value(127 + min(d, 15)), 0.f) & 0xFFFFu;
-            const uint32_t f = f1 | (f1 << 16);
-            uint32_t o[8];
-            const uint32_t* y = &x.x;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const uint32_t h = e4m3_to_f16x2((j & 1) ? y[j >> 1] >> 16 : y[j >> 1]);
-              const __half2 v = __hmul2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&f));
-              o[j] = *reinterpret_cast<const uint32_t*>(&v);
-            }
-            // the row's 16-byte chunks 2 chunk, 2 chunk + 1; half of the lanes start with the
-            // second, so that a quarter warp's stores hit all banks
-            uint8_t* dst = dst0 + r * 128 + (chunk >> 2) * C::kPanelBytes;
-            const int c0 = (2 * chunk) & 7, sw = D == 128 ? (chunk >> 2) & 1 : 0;
-            const uint4 lo = make_uint4(o[0], o[1], o[2], o[3]), hi = make_uint4(o[4], o[5], o[6], o[7]);
-            *reinterpret_cast<uint4*>(dst + (((c0 + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + (((c0 + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
-          }
+      for (int v = 0; v < 2; ++v) {
+        if (ok && n[v] > 0) ok = mbar_wait(&sh.c_empty[v], (n[v] - 1) & 1, abort_flag, st);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sh.c_full[v], kCodes + (v == 0 ? 2 : 1) * nvalid * R);
+        __syncwarp();
+        if (lane < boxes) tma_load_3d(sC + v * kCodes + lane * R * D, v == 0 ? tm_k : tm_v, &sh.c_full[v], 0, row, 0);
+        if (valid) {
+          if (v == 0) bulk_load(&sh.scales[0][lane * R], a.c.ks + row, R, &sh.c_full[0]);
+          bulk_load(&sh.scales[1 + v][lane * R], a.c.vs + row, R, &sh.c_full[v]);
         }
-        if (odd)
-          for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 7]) = seg[q] + 1;
-        fence_async_smem();
-        mbar_arrive(which == 0 ? &sh.k_full[s] : &sh.v_full[s]);
-        mbar_arrive(&sh.c_empty[which]);
-        stage(which);
+        ++n[v];
       }
     }
-    if (e.nu > 0)
-      for (int q = 0; q < nq; ++q) ++seg[q];
   }
-  // After a wait that ran out: copies in flight land before the shared memory goes away.
-  if (*abort_flag && loader && lane == 0)
-    for (int i = 0; i < 2; ++i)
-      if (nl[i] > 0) mbar_wait_drain(&sh.c_full[i], (nl[i] - 1) & 1, st);
   __syncwarp();
+  // After a wait that ran out: copies in flight land before the shared memory goes away.
+  if (*abort_flag && lane == 0)
+    for (int v = 0; v < 2; ++v)
+      if (n[v] > 0) mbar_wait_drain(&sh.c_full[v], (n[v] - 1) & 1, st);
+  __syncwarp();
+}
+
+// Warps 14 and 15 with an E4M3 cache: K into the ring, and each tile's factors.
+template <int D, int kStages>
+__device__ void expand_k_role(const TreeArgs& a, BigShared& sh, uint8_t* sK, const uint8_t* sC, Walk& w, int wi) {
+  const int lane = lane_id();
+  const DevStatus st{a.c.status, a.timeout_ns};
+  volatile int* abort_flag = &sh.abort_flag;
+  const Seg& e = w.e;
+  int n = 0;
+  uint32_t eref = 0;
+  bool ok = true;
+  while (ok && w.next(a)) {
+    for (int u = 0; u < e.nu && ok; ++u, ++n) {
+      const int s = n % kStages;
+      ok = mbar_wait(&sh.c_full[0], n & 1, abort_flag, st);
+      if (ok && n >= kStages) ok = mbar_wait(&sh.k_empty[s], ((n / kStages) - 1) & 1, abort_flag, st);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int keys = e.s.len + e.s.T - (e.kt0 + u) * kChunk;
+      const uint32_t ek = top_scale(sh.scales[0], keys);
+      const uint32_t en = next_eref(eref, top_scale(sh.scales[1], keys), u == 0);
+      if (wi == 0 && lane == 0) {
+        *reinterpret_cast<volatile float*>(&sh.kfac[n & 7]) = scale_value(ek);
+        *reinterpret_cast<volatile float*>(&sh.vfac[n & 7]) = u == 0 ? 1.f : exp2f((float)eref - (float)en);
+        *reinterpret_cast<volatile float*>(&sh.vref[n & 7]) = scale_value(en);
+      }
+      eref = en;
+      expand_tile<D, 2>(sC, sK + s * (kTile * D * 2), sh.scales[0], (int)ek, wi, false, 0);
+      fence_async_smem();
+      mbar_arrive(&sh.k_full[s]);
+      mbar_arrive(&sh.c_empty[0]);
+    }
+  }
 }
 
 // A Q row of bf16 pairs to fp16 (row_factor).  Returns the inverse factor, for the scores.
@@ -364,8 +376,8 @@ __global__ void __launch_bounds__(512, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&sh.k_full[s], kFp8 ? 96 : 1);
-      mbar_init(&sh.v_full[s], kFp8 ? 96 : 1);
+      mbar_init(&sh.k_full[s], kFp8 ? 64 : 1);
+      mbar_init(&sh.v_full[s], kFp8 ? 128 : 1);
       mbar_init(&sh.k_empty[s], 1);
       mbar_init(&sh.v_empty[s], 1);
       mbar_init(&sh.v_ok[s], 128);
@@ -381,7 +393,7 @@ __global__ void __launch_bounds__(512, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.c_full[i], 1);
-      mbar_init(&sh.c_empty[i], 96);
+      mbar_init(&sh.c_empty[i], i == 0 ? 64 : 128);
     }
     mbar_init(&sh.mma_done, 1);
     sh.abort_flag = 0;
@@ -406,8 +418,10 @@ __global__ void __launch_bounds__(512, 1)
     Walk w;
     w.start(cur, part);
     const Seg& e = w.e;
-    if (warp != C::kMmaWarp && kFp8) {
-      convert_role<D, kFp8, kFp16>(a, sh, sK, sV, sC, &tm_k, &tm_v, w, cur, part);
+    if (kFp8 && warp == C::kLoadWarp) {
+      stage_role<D>(a, sh, sC, &tm_k, &tm_v, w);
+    } else if (kFp8 && warp > C::kMmaWarp) {
+      expand_k_role<D, C::kStages>(a, sh, sK, sC, w, warp - C::kMmaWarp - 1);
     } else if (warp == C::kLoadWarp) {
       // ---------------------------------------------------------------- producer
       const int R = 1 << a.c.page_shift;                  // rows per box: one page
@@ -541,8 +555,27 @@ __global__ void __launch_bounds__(512, 1)
     Walk w;
     w.start(cur, part);
     const Seg& e = w.e;
+    uint32_t eref = 0;
     while (ok && w.next(a)) {
       const int nq = e.nrows > kTile ? 2 : 1;
+      auto expand_v = [&](int u) -> bool {                // tile u of the segment
+        const int n = nt + u, s = n % C::kStages;
+        bool go = mbar_wait(&sh.c_full[1], n & 1, abort_flag, st);
+        if (go && n >= C::kStages) go = mbar_wait(&sh.v_empty[s], ((n / C::kStages) - 1) & 1, abort_flag, st);
+        if (!__all_sync(0xffffffffu, go)) return false;
+        const int keys = e.s.len + e.s.T - (e.kt0 + u) * kChunk;
+        eref = next_eref(eref, top_scale(sh.scales[2], keys), u == 0);
+        if (expand_tile<D, 4>(sC + C::kCodes, sV + s * C::kTileBytes, sh.scales[2], (int)eref, wq,
+                              tail_tile(e, e.kt0 + u), keys))
+          for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 7]) = seg[q] + 1;
+        fence_async_smem();
+        mbar_arrive(&sh.v_full[s]);
+        mbar_arrive(&sh.c_empty[1]);
+        return true;
+      };
+      if constexpr (kFp8) {
+        if (e.nu > 0) ok = expand_v(0);
+      }
       for (int u = 0; u < e.nu && ok; ++u) {
         const int kt = e.kt0 + u;
         if (!kFp8 && tail_tile(e, kt)) {
@@ -582,23 +615,28 @@ __global__ void __launch_bounds__(512, 1)
           if (u > 0 && __any_sync(0xffffffffu, al != 1.f)) {
             tc_fence_after();
             const uint32_t tO = tmem + C::kOCol + q * D + lane_off;
+#pragma unroll 2
+            for (int cc = 0; cc < D; cc += 16) {          // 16 at a time: 32 spill beside the walk's state
+              uint32_t o[16];
+              tmem_ld16(tO + cc, o);
+              tmem_wait_ld();
+              reg_fence16(o);
 #pragma unroll
-            for (int cc = 0; cc < D; cc += 32) {
-              uint32_t o[32];
-              tmem_ld32_sync(tO + cc, o);
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
+              for (int i = 0; i < 16; i += 2) {
                 const float2 x = mul2(make_float2(__uint_as_float(o[i]), __uint_as_float(o[i + 1])), make_float2(al, al));
                 o[i] = __float_as_uint(x.x);
                 o[i + 1] = __float_as_uint(x.y);
               }
-              tmem_st32(tO + cc, o);
+              tmem_st16(tO + cc, o);
             }
             tmem_wait_st();
           }
           tc_fence_before();
           mbar_arrive(&sh.o_ready[q]);
           ++cq[q];
+        }
+        if constexpr (kFp8) {
+          if (ok && u + 1 < e.nu) ok = expand_v(u + 1);
         }
       }
       nt += e.nu;

@@ -3,8 +3,6 @@ and the host arithmetic of the serving helpers."""
 
 from __future__ import annotations
 
-import ctypes
-
 import numpy as np
 import pytest
 import torch
@@ -47,7 +45,7 @@ def _call(L, which, cache=None, **kw):
                  scale=0.125, workspace=FAKE, workspace_bytes=fa.fa_fwd_tree_workspace_bytes(4, 4, 2, 64), stream=None)
         cls, f = fa.TreeArgs, L.fa_fwd_tree
     a.update(kw)
-    return f(ctypes.byref(cls(c, *[a[n] for n, _ in cls._fields_[1:]])))
+    return f(bytes(cls(c, *[a[n] for n, _ in cls._fields_[1:]])))
 
 
 BAD_CACHE = [
@@ -120,6 +118,17 @@ def test_workspace_bytes(L):
     one = fa.fa_fwd_tree_workspace_bytes(1, 8, 2, 64)
     assert 0 < one <= fa.fa_fwd_tree_workspace_bytes(64, 8, 2, 64)
     assert fa.fa_fwd_tree_workspace_bytes(10 ** 6, 128, 1, 128) < 64 << 20   # does not grow with the call
+
+
+def test_packed_arguments_have_the_structs_layout():
+    c = _cache(k=11, v=12, page_table=13, pages=14)
+    for cls, pack, vals in ((fa.CacheAppendArgs, fa._pack_append, [1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11]),
+                            (fa.CacheReadArgs, fa._pack_read, [1, 2, 3, 4, 5, 6]),
+                            (fa.CacheKeepArgs, fa._pack_keep, [1, 2, 3, 4, 5]),
+                            (fa.TreeArgs, fa._pack_tree, [1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 15, 0.5, 17, 18, 19])):
+        got = cls.from_buffer_copy(bytes(c) + pack(*vals))
+        assert [getattr(got, n) for n, _ in cls._fields_[1:]] == vals
+        assert got.cache.k == 11 and got.cache.pages == 14
 
 
 def test_python_checks():
