@@ -102,13 +102,13 @@ __device__ __forceinline__ int row_factor(float amax) {
 
 // ------------------------------------------------------------------------------------
 // Schedule of the attention over the cache.  A unit is one (sequence, key head, row tile): rows are
-// the unit's (new token, query head of the group) pairs.  Its keys are cut into chunks of 128.
+// the unit's (new token, query head of the group) pairs.  Its keys are cut into chunks of 128 or 256.
 // All chunks of all units stand in one line -- sequences, in them key heads, in them row tiles,
 // in them chunks -- and CTA c of C takes the c-th of C equal parts, whatever units it cuts.
 // Every warp finds its part from the lengths on the device, so the host needs none of them.
 // ------------------------------------------------------------------------------------
 
-constexpr int kChunk = 128;      // keys
+constexpr int kChunk = 128;      // keys of a chunk of the tensor-memory kernel (the other has 128 or 256)
 constexpr int kTreeCtas = 148;   // most CTAs (one per SM)
 constexpr int kBigRows = 256;    // rows of a unit of the tensor-memory kernel
 
@@ -122,11 +122,13 @@ struct TreeArgs {
   const unsigned long long* mask;   // [total, words] or null
   float* part_o;                 // [C, 2, slot_rows, d] partial sums of units cut between CTAs
   float* part_ml;                // [C, 2, slot_rows, 2] their running max (log2 units) and sum
-  int4* meta;                    // [C] what CTA c leaves to the merge
+  int4* meta;                    // [C, 2] a cut unit that begins in CTA c: its last CTA (-1: none), rows, first
+                                 // token and key head; its first row
   long long q_tok, q_head, o_tok, o_head;   // strides in elements
   int total, Hq, G, words, max_new;
   int tile_rows;                 // rows of a row tile
   int slot_rows;                 // rows of a slot of part_o / part_ml: at least a unit's rows
+  int chunk_shift;               // log2 of a chunk's keys: 7 or 8
   unsigned long long timeout_ns;
   float scale_log2;
 };
@@ -152,7 +154,7 @@ __device__ __forceinline__ SeqView load_seq(const TreeArgs& a, int b, bool flag)
   s.len = len;
   s.cu0 = c0;
   s.RT = (int)(((long long)s.T * a.G + a.tile_rows - 1) / a.tile_rows);
-  s.KT = (int)((L + kChunk - 1) / kChunk);
+  s.KT = (int)((L - 1) >> a.chunk_shift) + 1;
   return s;
 }
 

@@ -60,22 +60,29 @@ __device__ __forceinline__ uint32_t expand2(uint32_t w) {
 template <int D, bool kFp8>
 struct SmallCfg {
   static constexpr int kEsz = kFp8 ? 1 : 2;
-  static constexpr int kHalf = 16 * D * kEsz;            // 16 rows of K (or V)
+  // Keys of a step.  32 where a row is at most 128 bytes: the fixed work of a step (its copies, row
+  // max and rescale) is then spent on 8 KB as with 16 rows of 256 bytes.
+  static constexpr int kKeys = D * kEsz <= 128 ? 32 : 16;
+  static constexpr int kChunkKeys = 8 * kKeys;           // a chunk: one step of each warp
+  static constexpr int kBoxes = kKeys / 16;              // copies of 16 rows (a page holds at least 16)
+  static constexpr int kBox = 16 * D * kEsz;
+  static constexpr int kHalf = kBoxes * kBox;            // K (or V) of a step
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = kFp8 ? 20480 / kStage : 24576 / kStage;
+  static constexpr int kStages = 24576 / kStage;
   static constexpr int kRing = 8 * kStages * kStage;     // all warps
-  static constexpr int kSlot = 16 * D * 4 + 128 + 16;    // one warp's O, m and l of 16 rows, V's exponent
-  static constexpr int kScales = kFp8 ? 8 * kStages * 32 : 0;
-  static constexpr int kSmem = kRing + 4 * kSlot + kScales + 1024;
+  static constexpr int kSlot = 16 * (D / 2) * 4 + 144;   // half of one warp's O, its m, l and E, of 16 rows
+  static constexpr int kScales = kFp8 ? 8 * kStages * 2 * kKeys : 0;
+  static constexpr int kSmem = kRing + 4 * kSlot + kScales;
   // bytes between 16-byte chunks' rows: 128-byte panels (64-byte rows for E4M3 at d = 64)
   static constexpr int kRowB = D * kEsz < 128 ? 64 : 128;
 };
 
-// Shared-memory offset of 16-byte chunk c of row r in a 16-row K or V stage as TMA wrote it.
+// Shared-memory offset of 16-byte chunk c of row r of K or V of a step as TMA wrote it.
 template <int D, bool kFp8>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
-  if constexpr (SmallCfg<D, kFp8>::kRowB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  else return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  const uint32_t box = (r >> 4) * SmallCfg<D, kFp8>::kBox;
+  if constexpr (SmallCfg<D, kFp8>::kRowB == 64) return box + (r & 15) * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  else return box + (c >> 3) * 2048 + (r & 15) * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // kFp16: type of q and o.  A 16-bit cache's products are in that type.  An E4M3 cache's are in fp16, which
@@ -90,16 +97,20 @@ __global__ void __launch_bounds__(256, 1)
                       const TreeArgs a) {
   using C = SmallCfg<D, kFp8>;
   constexpr int kNT = D / 8;                              // 8-column tiles of O
+  constexpr int kST = C::kKeys / 8;                       // 8-key tiles of S
+  constexpr int kG = C::kKeys / 16;                       // 16-key groups
   constexpr bool kMma16 = kFp8 || kFp16;                  // products in fp16
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ uint64_t full[8][C::kStages];
   __shared__ int abort_flag;
-  const uint32_t pad = (1024u - (smem_addr(smem_raw) & 1023u)) & 1023u;
-  uint8_t* base = smem_raw + pad;
+  if ((smem_addr(smem_raw) & 1023u) != 0) {               // the copies' swizzle needs it
+    if (threadIdx.x == 0) atomicCAS(a.c.status, 0, kDevBadState);
+    return;
+  }
   const int warp = warp_id(), lane = lane_id();
-  uint8_t* ring = base + warp * C::kStages * C::kStage;
-  uint8_t* slots = base + C::kRing;
-  uint8_t* scales = slots + 4 * C::kSlot + warp * C::kStages * 32;
+  uint8_t* ring = smem_raw + warp * C::kStages * C::kStage;
+  uint8_t* slots = smem_raw + C::kRing;
+  uint8_t* scales = slots + 4 * C::kSlot + warp * C::kStages * 2 * C::kKeys;
   const DevStatus st{a.c.status, a.timeout_ns};
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -111,60 +122,82 @@ __global__ void __launch_bounds__(256, 1)
     prefetch_tmap(&tm_v);
   }
   fence_barrier_init();
-  __syncthreads();
 
   const long long total = total_chunks(a, blockIdx.x == 0 && warp == 0);
   const Part part = part_of(total, blockIdx.x, gridDim.x);
-  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   if (part.n == 0) return;
   Cursor rd = locate(a, part.lo), ld = rd;
   int rd_left = part.n, ld_left = part.n;
+  __syncthreads();
 
   // ---------------------------------------------------------------- loads
-  // A step is loaded when its first key exists and some row of the tile may see it.
-  auto wanted = [&](const Cursor& c) { return c.kt * kChunk + warp * 16 <= c.last; };
-  int issued = 0, used = 0;                               // stages filled and consumed
-  bool ok = true;
+  // A step is loaded when its first key exists and some row of the tile may see it.  `ld` stands at
+  // the next step to load, whose page ids (lane i: box i) are on their way since the last.
+  auto wanted = [&](const Cursor& c) { return c.kt * C::kChunkKeys + warp * C::kKeys <= c.last; };
+  int page = 0;
   auto advance = [&](Cursor& c, int& left) {
     --left;
     if (++c.kt < c.s.KT) return;
     if (left > 0) next_unit(a, c);
   };
-  auto fill = [&]() {                                     // start the next wanted step's copy, if any
-    while (ld_left > 0) {
-      const bool w = wanted(ld);
-      if (w) {
-        if (lane == 0) {
-          const int p0 = ld.kt * kChunk + warp * 16;
-          long long row = slot_row(a.c, ld.b, ld.h, p0);
-          if (row < 0) row = 0;                           // flagged; stay inside the cache
-          const int stg = issued % C::kStages;
-          uint64_t* bar = &full[warp][stg];
-          mbar_arrive_expect_tx(bar, C::kStage + (kFp8 ? 32 : 0));
-          tma_load_3d(ring + stg * C::kStage, &tm_k, bar, 0, (int)row, 0);
-          tma_load_3d(ring + stg * C::kStage + C::kHalf, &tm_v, bar, 0, (int)row, 0);
-          if constexpr (kFp8) {
-            bulk_load(scales + stg * 32, a.c.ks + row, 16, bar);
-            bulk_load(scales + stg * 32 + 16, a.c.vs + row, 16, bar);
-          }
-        }
-        ++issued;
-      }
-      advance(ld, ld_left);
-      if (w) return;
+  auto look_up = [&]() {
+    while (ld_left > 0 && !wanted(ld)) advance(ld, ld_left);
+    if (ld_left > 0 && lane < C::kBoxes) {
+      const int pos = ld.kt * C::kChunkKeys + warp * C::kKeys + 16 * lane;
+      if (pos < ld.s.len + ld.s.T) page = a.c.table[(long long)ld.b * a.c.table_stride + (pos >> a.c.page_shift)];
     }
   };
-  for (int i = 0; i < C::kStages; ++i) fill();
+  int fs = 0;                                             // stage to fill
+  auto fill = [&]() {                                     // start the next wanted step's copies, if any
+    if (ld_left <= 0) return;
+    const int p0 = ld.kt * C::kChunkKeys + warp * C::kKeys, end = ld.s.len + ld.s.T;
+    uint64_t* bar = &full[warp][fs];
+    if (lane == 0) {
+      const int boxes = min(C::kBoxes, (end - p0 + 15) >> 4);     // that hold keys: scales come with them
+      mbar_arrive_expect_tx(bar, C::kStage + (kFp8 ? boxes * 32 : 0));
+    }
+    __syncwarp();
+    if (lane < C::kBoxes) {
+      const int pos = p0 + 16 * lane;
+      int row;
+      if (pos >= end) {                                   // past the end: a row behind the tensor reads as zeros
+        row = (a.c.pages * a.c.Hk) << a.c.page_shift;
+      } else {
+        if ((unsigned)page >= (unsigned)a.c.pages) {
+          flag_range(a.c);
+          page = 0;                                       // stay inside the cache
+        }
+        row = ((page * a.c.Hk + ld.h) << a.c.page_shift) + (pos & ((1 << a.c.page_shift) - 1));
+      }
+      uint8_t* dst = ring + fs * C::kStage + lane * C::kBox;
+      tma_load_3d(dst, &tm_k, bar, 0, row, 0);
+      tma_load_3d(dst + C::kHalf, &tm_v, bar, 0, row, 0);
+      if constexpr (kFp8) {
+        if (pos < end) {
+          bulk_load(scales + fs * 2 * C::kKeys + 16 * lane, a.c.ks + row, 16, bar);
+          bulk_load(scales + (fs * 2 + 1) * C::kKeys + 16 * lane, a.c.vs + row, 16, bar);
+        }
+      }
+    }
+    fs = fs + 1 == C::kStages ? 0 : fs + 1;
+    advance(ld, ld_left);
+    look_up();
+  };
+  look_up();
+  int issued = 0;
+  for (int i = 0; i < C::kStages && ld_left > 0; ++i, ++issued) fill();
 
   // ---------------------------------------------------------------- segments
   const int r0 = lane >> 2, tq = lane & 3;                // fragment row and column quad
+  int us = 0, uphase = 0, used = 0;                       // stage to use, its parity
+  bool ok = true;
   while (rd_left > 0) {
     const SeqView s = rd.s;
     const int h = rd.h;
     const int row0 = (rd.u - h * s.RT) * a.tile_rows;
     const int nrows = (int)min((long long)a.tile_rows, (long long)s.T * a.G - row0);
     const bool from_start = rd.kt == 0;
-    const int seg_unit = rd.u, seg_b = rd.b;
     const long long seg_g = part.lo + (part.n - rd_left);  // the segment's first chunk in the line
 
     // Q fragments; rows past the unit's last read the last one (never stored)
@@ -226,258 +259,265 @@ __global__ void __launch_bounds__(256, 1)
       m[mt][0] = m[mt][1] = -INFINITY;
       l[mt][0] = l[mt][1] = 0.f;
     }
-
     int eref = kNoScale;                                  // E4M3: E (as a scale code) of what O holds
 
     // ------------------------------------------------------------ the segment's steps
-    bool more = true;
-    while (more) {
-      if (wanted(rd)) {
-        const int stg = used % C::kStages;
-        if (ok) ok = mbar_wait(&full[warp][stg], (used / C::kStages) & 1, &abort_flag, st);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-          const uint8_t* sk = ring + stg * C::kStage;
-          const uint32_t ak = smem_addr(sk), av = ak + C::kHalf;
-          const int p0 = rd.kt * kChunk + warp * 16;
-          // ---- S = Q K^T, 16 * kMT rows x 16 keys
-          float sc[kMT][2][4];
+    // Unit, sequence and head stay; only kt moves until the unit or the part ends.
+    const int kt_end = (int)min((long long)s.KT, (long long)rd.kt + rd_left);
+    for (int kt = rd.kt; kt < kt_end; ++kt) {
+      const int p0 = kt * C::kChunkKeys + warp * C::kKeys;
+      if (p0 > rd.last) continue;
+      if (ok) ok = mbar_wait(&full[warp][us], uphase, &abort_flag, st);
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) {
+        const uint8_t* sk = ring + us * C::kStage;
+        const uint32_t ak = smem_addr(sk), av = ak + C::kHalf;
+        const int end = s.len + s.T - p0;                 // keys of the step from here on do not exist
+        const bool masked = p0 + C::kKeys > s.len;
+        // ---- S = Q K^T, 16 * kMT rows x kKeys keys
+        float sc[kMT][kST][4];
 #pragma unroll
-          for (int mt = 0; mt < kMT; ++mt)
+        for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
+          for (int j = 0; j < kST; ++j)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) sc[mt][j][i] = 0.f;
-          float kf[2][2] = {{1.f, 1.f}, {1.f, 1.f}}, vf[2][2] = {{1.f, 1.f}, {1.f, 1.f}};
-          const bool masked = p0 + 16 > s.len;
-          if constexpr (kFp8) {
-            const uint8_t* sp = scales + stg * 32;
+            for (int i = 0; i < 4; ++i) sc[mt][j][i] = 0.f;
+        float kf[kST][2], vf[kST][2];
+        if constexpr (kFp8) {
+          const uint8_t* sp = scales + us * 2 * C::kKeys;
 #pragma unroll
-            for (int c = 0; c < D / 16; c += 2) {
+          for (int c = 0; c < D / 16; c += 2)
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
               uint32_t kr[4];
-              ldsm4(ak + swz<D, true>((lane & 7) + ((lane >> 3) & 1) * 8, c + (lane >> 4)), kr);
+              ldsm4(ak + swz<D, true>(16 * g + (lane & 7) + ((lane >> 3) & 1) * 8, c + (lane >> 4)), kr);
 #pragma unroll
               for (int j = 0; j < 2; ++j) {
                 const uint32_t a0 = expand2<0, 1>(kr[j]), a1 = expand2<2, 3>(kr[j]);
                 const uint32_t b0 = expand2<0, 1>(kr[2 + j]), b1 = expand2<2, 3>(kr[2 + j]);
 #pragma unroll
                 for (int mt = 0; mt < kMT; ++mt) {
-                  mma16816<true>(sc[mt][j], qf[mt][c], a0, a1);
-                  mma16816<true>(sc[mt][j], qf[mt][c + 1], b0, b1);
+                  mma16816<true>(sc[mt][2 * g + j], qf[mt][c], a0, a1);
+                  mma16816<true>(sc[mt][2 * g + j], qf[mt][c + 1], b0, b1);
                 }
               }
             }
-            // the largest of V's scales among the keys that exist
-            const uint32_t top = __reduce_max_sync(0xffffffffu, lane < 16 && p0 + lane < s.len + s.T ? sp[16 + (lane & 15)] : 0u);
-            if ((int)top > eref + 15) {
-              const int e = (int)top - 8;
-              if (eref != kNoScale) {                     // rare: a first scale far above the ones before
-                const float f = exp2f((float)(eref - e));
-#pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                  for (int n = 0; n < kNT; ++n)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
-              }
-              eref = e;
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const int wk = *reinterpret_cast<const uint16_t*>(sp + 8 * j + 2 * tq);
-              const int wv = *reinterpret_cast<const uint16_t*>(sp + 16 + 8 * j + 2 * tq);
-              kf[j][0] = scale_value(wk & 0xFF);
-              kf[j][1] = scale_value(wk >> 8);
-              vf[j][0] = scale_value(max((wv & 0xFF) + 127 - eref, 0));
-              vf[j][1] = scale_value(max((wv >> 8) + 127 - eref, 0));
-            }
-          } else {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              uint32_t kr[4];
-              ldsm4(ak + swz<D, false>((lane & 7) + (lane >> 4) * 8, 2 * kk + ((lane >> 3) & 1)), kr);
-#pragma unroll
-              for (int mt = 0; mt < kMT; ++mt) {
-                mma16816<kFp16>(sc[mt][0], qf[mt][kk], kr[0], kr[1]);
-                mma16816<kFp16>(sc[mt][1], qf[mt][kk], kr[2], kr[3]);
-              }
-            }
-          }
-          // ---- scale, mask, online softmax
-          uint32_t pf[kMT][4];
-          unsigned see[kMT][2];                           // bit 2j + i: key 8j + 2 tq + i is visible
-#pragma unroll
-          for (int mt = 0; mt < kMT; ++mt) {
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-              float x[2][2];
-              see[mt][hf] = 0xF;
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) x[j][i] = sc[mt][j][2 * hf + i] * (kFp8 ? sl2[mt][hf] * kf[j][i] : sl2[mt][hf]);
-              if (masked) {
-                const int t = tok[mt][hf];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                  for (int i = 0; i < 2; ++i) {
-                    const int n = p0 + 8 * j + 2 * tq + i - s.len;     // new token of this key
-                    bool vis = n < 0;
-                    if (n >= 0 && n < s.T) {
-                      if (a.mask == nullptr) vis = n <= t;
-                      else vis = (n >> 6) < a.words &&
-                                 ((a.mask[(long long)(s.cu0 + t) * a.words + (n >> 6)] >> (n & 63)) & 1);
-                    }
-                    if (!vis) {
-                      x[j][i] = -INFINITY;
-                      see[mt][hf] &= ~(1u << (2 * j + i));
-                    }
-                  }
-              }
-              float mx = fmaxf(fmaxf(x[0][0], x[0][1]), fmaxf(x[1][0], x[1][1]));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-              const float mn = fmaxf(m[mt][hf], mx);
-              const float neg = mn == -INFINITY ? 0.f : -mn;
-              const float al = ex2(m[mt][hf] + neg);      // 0 while m = -inf
-              m[mt][hf] = mn;
-              float sum = 0.f;
-              float p[2][2];
-#pragma unroll
-              for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  p[j][i] = ex2(x[j][i] + neg);
-                  sum += p[j][i];
-                }
-              l[mt][hf] = l[mt][hf] * al + sum;
-              if (__any_sync(0xffffffffu, al != 1.f)) {
-#pragma unroll
-                for (int n = 0; n < kNT; ++n) {
-                  o[mt][n][2 * hf] *= al;
-                  o[mt][n][2 * hf + 1] *= al;
-                }
-              }
-              // P to 16 bits, one rounding of at most half a step (the row sum keeps 32 bits); a
-              // masked key's scale may be anything, so its zero is not multiplied
-#pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                if constexpr (kFp8) {
-#pragma unroll
-                  for (int i = 0; i < 2; ++i) p[j][i] = masked && !((see[mt][hf] >> (2 * j + i)) & 1) ? 0.f : p[j][i] * vf[j][i];
-                }
-                pf[mt][hf + 2 * j] = pack2<kMma16>(p[j][0], p[j][1]);
-              }
-            }
-          }
-          // ---- O += P V
-          // Past the sequence's last key the page holds anything: those rows of V count as zero.
-          uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
-          if (masked) {
-            const int end = s.len + s.T - p0 - 2 * tq;     // keys from here on do not exist
-            keep0 = (end > 0 ? 0xFFFFu : 0u) | (end > 1 ? 0xFFFF0000u : 0u);
-            keep1 = (end > 8 ? 0xFFFFu : 0u) | (end > 9 ? 0xFFFF0000u : 0u);
-          }
-          // V of columns 32 c .. 32 c + 31 (E4M3) or 16 c .. 16 c + 15: kVT tiles of 8 columns
-          constexpr int kVT = kFp8 ? 4 : 2;
-          auto vfrag = [&](int c, uint32_t (&b)[kVT][2]) {
-            uint32_t vr[4];
-            if constexpr (kFp8) {
-              ldsm4t(av + swz<D, true>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * c + (lane >> 4)), vr);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {               // keys 8 (i % 2) .., columns 16 (i / 2) ..
-                b[2 * (i >> 1)][i & 1] = expand2<0, 2>(vr[i]);
-                b[2 * (i >> 1) + 1][i & 1] = expand2<1, 3>(vr[i]);
-              }
-            } else {
-              ldsm4t(av + swz<D, false>((lane & 7) + ((lane >> 3) & 1) * 8, 2 * c + (lane >> 4)), vr);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) b[i >> 1][i & 1] = vr[i];
-            }
-          };
-          // The products one by one, visible keys only.
-          auto one_by_one = [&]() {
-            const int live = min(16, s.len + s.T - p0);
-            for (int key = 0; key < live; ++key) {
-              const int src = (lane & ~3) | ((key & 7) >> 1), j = key >> 3, i = key & 1;
-              float w[kMT][2];
-              bool v[kMT][2];
+          // the largest of V's scales among the keys that exist
+          const uint32_t top = __reduce_max_sync(0xffffffffu, lane < min(C::kKeys, end) ? sp[C::kKeys + (lane & (C::kKeys - 1))] : 0u);
+          if ((int)top > eref + 15) {
+            const int e = (int)top - 8;
+            if (eref != kNoScale) {                       // rare: a scale far above the ones before
+              const float f = exp2f((float)(eref - e));
 #pragma unroll
               for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) {
-                  const float2 f = unpack2<kMma16>(__shfl_sync(0xffffffffu, j ? pf[mt][hf + 2] : pf[mt][hf], src));
-                  w[mt][hf] = i ? f.y : f.x;
-                  v[mt][hf] = (__shfl_sync(0xffffffffu, see[mt][hf], src) >> (2 * j + i)) & 1;
-                }
+                for (int n = 0; n < kNT; ++n)
 #pragma unroll
-              for (int n = 0; n < kNT; ++n)
+                  for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
+            }
+            eref = e;
+          }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                  float x;                                // V[key][column of accumulator (n, e)]
-                  if constexpr (kFp8) {
-                    const int col = 16 * (n >> 1) + 4 * tq + 2 * e + (n & 1);
-                    x = unpack2<true>(e4m3_to_f16x2(sk[C::kHalf + swz<D, true>(key, col >> 4) + (col & 15)])).x;
-                  } else {
-                    const int col = 8 * n + 2 * tq + e;
-                    x = unpack2<kFp16>(*reinterpret_cast<const uint16_t*>(sk + C::kHalf + swz<D, false>(key, col >> 3) +
-                                                                          2 * (col & 7))).x;
+          for (int j = 0; j < kST; ++j) {
+            const int wk = *reinterpret_cast<const uint16_t*>(sp + 8 * j + 2 * tq);
+            const int wv = *reinterpret_cast<const uint16_t*>(sp + C::kKeys + 8 * j + 2 * tq);
+            kf[j][0] = scale_value(wk & 0xFF);
+            kf[j][1] = scale_value(wk >> 8);
+            vf[j][0] = scale_value(max((wv & 0xFF) + 127 - eref, 0));
+            vf[j][1] = scale_value(max((wv >> 8) + 127 - eref, 0));
+          }
+        } else {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              uint32_t kr[4];
+              ldsm4(ak + swz<D, false>(16 * g + (lane & 7) + (lane >> 4) * 8, 2 * kk + ((lane >> 3) & 1)), kr);
+#pragma unroll
+              for (int mt = 0; mt < kMT; ++mt) {
+                mma16816<kFp16>(sc[mt][2 * g], qf[mt][kk], kr[0], kr[1]);
+                mma16816<kFp16>(sc[mt][2 * g + 1], qf[mt][kk], kr[2], kr[3]);
+              }
+            }
+        }
+        // ---- scale, mask, online softmax
+        uint32_t pf[kMT][kG][4];
+        unsigned see[kMT][2];                             // bit 2j + i: key 8j + 2 tq + i is visible
+#pragma unroll
+        for (int mt = 0; mt < kMT; ++mt) {
+#pragma unroll
+          for (int hf = 0; hf < 2; ++hf) {
+            float x[kST][2];
+            see[mt][hf] = 0xFFu;
+#pragma unroll
+            for (int j = 0; j < kST; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) x[j][i] = sc[mt][j][2 * hf + i] * (kFp8 ? sl2[mt][hf] * kf[j][i] : sl2[mt][hf]);
+            if (masked) {
+              const int t = tok[mt][hf];
+#pragma unroll
+              for (int j = 0; j < kST; ++j)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const int n = p0 + 8 * j + 2 * tq + i - s.len;     // new token of this key
+                  bool vis = n < 0;
+                  if (n >= 0 && n < s.T) {
+                    if (a.mask == nullptr) vis = n <= t;
+                    else vis = (n >> 6) < a.words &&
+                               ((a.mask[(long long)(s.cu0 + t) * a.words + (n >> 6)] >> (n & 63)) & 1);
                   }
-#pragma unroll
-                  for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf)
-                      if (v[mt][hf]) o[mt][n][2 * hf + e] += w[mt][hf] * x;
+                  if (!vis) {
+                    x[j][i] = -INFINITY;
+                    see[mt][hf] &= ~(1u << (2 * j + i));
+                  }
                 }
             }
-          };
-          // A masked product is 0 * v, which is not 0 where v is not finite: a step of new tokens
-          // whose values are not all finite is done one by one.
-          bool apart = false;
-          if (masked) {
-            bool bad = false;
+            float mx = fmaxf(x[0][0], x[0][1]);
 #pragma unroll
-            for (int c = 0; c < kNT / kVT; ++c) {
+            for (int j = 1; j < kST; ++j) mx = max3f(mx, x[j][0], x[j][1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            const float mn = fmaxf(m[mt][hf], mx);
+            const float neg = mn == -INFINITY ? 0.f : -mn;
+            const float al = ex2(m[mt][hf] + neg);        // 0 while m = -inf
+            m[mt][hf] = mn;
+            float sum = 0.f;
+            float p[kST][2];
+#pragma unroll
+            for (int j = 0; j < kST; ++j)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                p[j][i] = ex2(x[j][i] + neg);
+                sum += p[j][i];
+              }
+            l[mt][hf] = l[mt][hf] * al + sum;
+            if (__any_sync(0xffffffffu, al != 1.f)) {
+#pragma unroll
+              for (int n = 0; n < kNT; ++n) {
+                o[mt][n][2 * hf] *= al;
+                o[mt][n][2 * hf + 1] *= al;
+              }
+            }
+            // P to 16 bits, one rounding of at most half a step (the row sum keeps 32 bits); a
+            // masked key's scale may be anything, so its zero is not multiplied
+#pragma unroll
+            for (int j = 0; j < kST; ++j) {
+              if constexpr (kFp8) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) p[j][i] = masked && !((see[mt][hf] >> (2 * j + i)) & 1) ? 0.f : p[j][i] * vf[j][i];
+              }
+              pf[mt][j >> 1][hf + 2 * (j & 1)] = pack2<kMma16>(p[j][0], p[j][1]);
+            }
+          }
+        }
+        // ---- O += P V
+        // V of a 16-key group, columns 32 c .. 32 c + 31 (E4M3) or 16 c .. 16 c + 15: kVT tiles of 8
+        constexpr int kVT = kFp8 ? 4 : 2;
+        auto vfrag = [&](int g, int c, uint32_t (&b)[kVT][2]) {
+          uint32_t vr[4];
+          ldsm4t(av + swz<D, kFp8>(16 * g + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * c + (lane >> 4)), vr);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {                   // keys 8 (i % 2) .., 16-byte chunk i / 2
+            if constexpr (kFp8) {
+              b[2 * (i >> 1)][i & 1] = expand2<0, 2>(vr[i]);
+              b[2 * (i >> 1) + 1][i & 1] = expand2<1, 3>(vr[i]);
+            } else {
+              b[i >> 1][i & 1] = vr[i];
+            }
+          }
+        };
+        // Past the sequence's last key the page holds anything: those rows of V count as zero.
+        auto keep = [&](int g, int i) -> uint32_t {       // of the keys in half i of group g's fragments
+          const int k = end - 16 * g - 2 * tq - 8 * i;
+          return (k > 0 ? 0xFFFFu : 0u) | (k > 1 ? 0xFFFF0000u : 0u);
+        };
+        // A masked product is 0 * v, which is not 0 where v is not finite: a step of new tokens
+        // whose values are not all finite makes its products one by one, visible keys only.
+        bool apart = false;
+        if (masked) {
+          bool bad = false;
+#pragma unroll 1
+          for (int c = 0; c < kNT / kVT; ++c)
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
               uint32_t b[kVT][2];
-              vfrag(c, b);
+              vfrag(g, c, b);
 #pragma unroll
               for (int i = 0; i < 2 * kVT; ++i) {
-                const uint32_t w = b[i >> 1][i & 1] & ((i & 1) ? keep1 : keep0);
+                const uint32_t w = b[i >> 1][i & 1] & keep(g, i & 1);
                 const uint32_t e = kMma16 ? 0x7C00u : 0x7F80u;
                 bad |= (w & e) == e || ((w >> 16) & e) == e;
               }
             }
-            apart = __any_sync(0xffffffffu, bad);
-          }
-          if (apart) {
-            one_by_one();
-          } else {
+          apart = __any_sync(0xffffffffu, bad);
+        }
+        if (apart) {
+#pragma unroll 1
+          for (int key = 0; key < min(C::kKeys, end); ++key) {
+            const int src = (lane & ~3) | ((key & 7) >> 1), j = key >> 3, i = key & 1;
+            float w[kMT][2];
+            bool v[kMT][2];
 #pragma unroll
-            for (int c = 0; c < kNT / kVT; ++c) {
-              uint32_t b[kVT][2];
-              vfrag(c, b);
+            for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
-              for (int i = 0; i < kVT; ++i) {
-                if (masked) {
-                  b[i][0] &= keep0;
-                  b[i][1] &= keep1;
+              for (int hf = 0; hf < 2; ++hf) {
+                uint32_t pw = pf[mt][0][hf];              // tile j's pair of this lane's row
+#pragma unroll
+                for (int k = 1; k < kST; ++k)
+                  if (j == k) pw = pf[mt][k >> 1][hf + 2 * (k & 1)];
+                const float2 f = unpack2<kMma16>(__shfl_sync(0xffffffffu, pw, src));
+                w[mt][hf] = i ? f.y : f.x;
+                v[mt][hf] = (__shfl_sync(0xffffffffu, see[mt][hf], src) >> (2 * j + i)) & 1;
+              }
+#pragma unroll
+            for (int n = 0; n < kNT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x;                                  // V[key][column of accumulator (n, e)]
+                if constexpr (kFp8) {
+                  const int col = 16 * (n >> 1) + 4 * tq + 2 * e + (n & 1);
+                  x = unpack2<true>(e4m3_to_f16x2(sk[C::kHalf + swz<D, true>(key, col >> 4) + (col & 15)])).x;
+                } else {
+                  const int col = 8 * n + 2 * tq + e;
+                  x = unpack2<kFp16>(*reinterpret_cast<const uint16_t*>(sk + C::kHalf + swz<D, false>(key, col >> 3) +
+                                                                        2 * (col & 7))).x;
                 }
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) mma16816<kMma16>(o[mt][kVT * c + i], pf[mt], b[i][0], b[i][1]);
+                for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                  for (int hf = 0; hf < 2; ++hf)
+                    if (v[mt][hf]) o[mt][n][2 * hf + e] += w[mt][hf] * x;
               }
-            }
           }
+        } else {
+#pragma unroll
+          for (int c = 0; c < kNT / kVT; ++c)
+#pragma unroll
+            for (int g = 0; g < kG; ++g) {
+              uint32_t b[kVT][2];
+              vfrag(g, c, b);
+              if (masked) {
+#pragma unroll
+                for (int i = 0; i < 2 * kVT; ++i) b[i >> 1][i & 1] &= keep(g, i & 1);
+              }
+#pragma unroll
+              for (int i = 0; i < kVT; ++i)
+#pragma unroll
+                for (int mt = 0; mt < kMT; ++mt) mma16816<kMma16>(o[mt][kVT * c + i], pf[mt][g], b[i][0], b[i][1]);
+            }
         }
-        ++used;
-        __syncwarp();                                     // the stage has been read: refill it
-        if (ok) fill();
       }
-      const int kt = rd.kt + 1;
-      more = kt < s.KT && rd_left > 1;
-      advance(rd, rd_left);
+      us = us + 1 == C::kStages ? 0 : us + 1;
+      if (us == 0) uphase ^= 1;
+      ++used;
+      __syncwarp();                                       // the stage has been read: refill it
+      if (ok && ld_left > 0) {
+        fill();
+        ++issued;
+      }
     }
-    const bool to_end = rd_left > 0 || rd.kt >= s.KT;
+    const bool to_end = kt_end == s.KT;
+    rd_left -= kt_end - rd.kt;
 
     // ------------------------------------------------------------ merge of the eight warps
 #pragma unroll
@@ -489,52 +529,63 @@ __global__ void __launch_bounds__(256, 1)
       }
       int em = eref;                                      // E of this row block's O
       for (int half = 4; half > 0; half >>= 1) {
-        __syncthreads();
-        if (warp >= half && warp < 2 * half) {
-          uint8_t* sl = slots + (warp - half) * C::kSlot;
-          float4* so = reinterpret_cast<float4*>(sl);
+        float fa[2], fb[2];
 #pragma unroll
-          for (int n = 0; n < kNT; ++n) so[n * 32 + lane] = make_float4(o[mt][n][0], o[mt][n][1], o[mt][n][2], o[mt][n][3]);
-          float* sm = reinterpret_cast<float*>(sl + 16 * D * 4);
-          if (tq == 0) {
-            sm[r0] = m[mt][0];
-            sm[r0 + 8] = m[mt][1];
-            sm[16 + r0] = l[mt][0];
-            sm[24 + r0] = l[mt][1];
-          }
-          if (kFp8 && lane == 0) reinterpret_cast<int*>(sm)[32] = em;
-        }
-        __syncthreads();
-        if (warp < half) {
-          const uint8_t* sl = slots + warp * C::kSlot;
-          const float4* so = reinterpret_cast<const float4*>(sl);
-          const float* sm = reinterpret_cast<const float*>(sl + 16 * D * 4);
-          float fa[2], fb[2], ga = 1.f, gb = 1.f;         // factors of O beside the maxima's
-          if constexpr (kFp8) {
-            const int eb = reinterpret_cast<const int*>(sm)[32], en = max(em, eb);
-            ga = exp2f((float)(em - en));
-            gb = exp2f((float)(eb - en));
-            em = en;
-          }
+        for (int part2 = 0; part2 < 2; ++part2) {         // half of the columns at a time
+          constexpr int kH = kNT / 2;
+          __syncthreads();
+          if (warp >= half && warp < 2 * half) {
+            uint8_t* sl = slots + (warp - half) * C::kSlot;
+            float4* so = reinterpret_cast<float4*>(sl);
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            const float mb = sm[r0 + 8 * hf], lb = sm[16 + r0 + 8 * hf];
-            const float mn = fmaxf(m[mt][hf], mb);
-            const float neg = mn == -INFINITY ? 0.f : -mn;
-            fa[hf] = ex2(m[mt][hf] + neg);
-            fb[hf] = ex2(mb + neg);
-            m[mt][hf] = mn;
-            l[mt][hf] = l[mt][hf] * fa[hf] + lb * fb[hf];
-            fa[hf] *= ga;
-            fb[hf] *= gb;
+            for (int n = 0; n < kH; ++n) {
+              const float (&x)[4] = o[mt][part2 * kH + n];
+              so[n * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
+            }
+            float* sm = reinterpret_cast<float*>(sl + 16 * (D / 2) * 4);
+            if (part2 == 0 && tq == 0) {
+              sm[r0] = m[mt][0];
+              sm[r0 + 8] = m[mt][1];
+              sm[16 + r0] = l[mt][0];
+              sm[24 + r0] = l[mt][1];
+            }
+            if (kFp8 && part2 == 0 && lane == 0) reinterpret_cast<int*>(sm)[32] = em;
           }
+          __syncthreads();
+          if (warp < half) {
+            const uint8_t* sl = slots + warp * C::kSlot;
+            const float4* so = reinterpret_cast<const float4*>(sl);
+            if (part2 == 0) {
+              const float* sm = reinterpret_cast<const float*>(sl + 16 * (D / 2) * 4);
+              float ga = 1.f, gb = 1.f;                   // factors of O beside the maxima's
+              if constexpr (kFp8) {
+                const int eb = reinterpret_cast<const int*>(sm)[32], en = max(em, eb);
+                ga = exp2f((float)(em - en));
+                gb = exp2f((float)(eb - en));
+                em = en;
+              }
 #pragma unroll
-          for (int n = 0; n < kNT; ++n) {
-            const float4 w = so[n * 32 + lane];
-            o[mt][n][0] = o[mt][n][0] * fa[0] + w.x * fb[0];
-            o[mt][n][1] = o[mt][n][1] * fa[0] + w.y * fb[0];
-            o[mt][n][2] = o[mt][n][2] * fa[1] + w.z * fb[1];
-            o[mt][n][3] = o[mt][n][3] * fa[1] + w.w * fb[1];
+              for (int hf = 0; hf < 2; ++hf) {
+                const float mb = sm[r0 + 8 * hf], lb = sm[16 + r0 + 8 * hf];
+                const float mn = fmaxf(m[mt][hf], mb);
+                const float neg = mn == -INFINITY ? 0.f : -mn;
+                fa[hf] = ex2(m[mt][hf] + neg);
+                fb[hf] = ex2(mb + neg);
+                m[mt][hf] = mn;
+                l[mt][hf] = l[mt][hf] * fa[hf] + lb * fb[hf];
+                fa[hf] *= ga;
+                fb[hf] *= gb;
+              }
+            }
+#pragma unroll
+            for (int n = 0; n < kH; ++n) {
+              const float4 w = so[n * 32 + lane];
+              float (&x)[4] = o[mt][part2 * kH + n];
+              x[0] = x[0] * fa[0] + w.x * fb[0];
+              x[1] = x[1] * fa[0] + w.y * fb[0];
+              x[2] = x[2] * fa[1] + w.z * fb[1];
+              x[3] = x[3] * fa[1] + w.w * fb[1];
+            }
           }
         }
       }
@@ -547,7 +598,10 @@ __global__ void __launch_bounds__(256, 1)
     if (warp == 0) {
       const bool whole = from_start && to_end;
       const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
-      if (lane == 0 && from_start && !to_end) a.meta[blockIdx.x] = make_int4(seg_b, seg_unit, owner_cta(total, seg_g + s.KT - 1, gridDim.x), 0);
+      if (lane == 0 && from_start && !to_end) {
+        a.meta[2 * blockIdx.x] = make_int4(owner_cta(total, seg_g + s.KT - 1, gridDim.x), nrows, s.cu0, h);
+        a.meta[2 * blockIdx.x + 1] = make_int4(row0, 0, 0, 0);
+      }
 #pragma unroll
       for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
@@ -598,6 +652,7 @@ __global__ void __launch_bounds__(256, 1)
           }
         }
     }
+    if (rd_left > 0) next_unit(a, rd);
   }
   // A wait that ran out left copies in flight: let them land before the shared memory goes away.
   if (!ok && lane == 0)
@@ -615,15 +670,11 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   constexpr int kV = D / 32;                              // columns per lane
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, lane = lane_id();
-  const int4 me = a.meta[c];
-  if (me.x < 0) return;
-  const SeqView s = load_seq(a, me.x, false);
-  const int h = me.y / s.RT, rt = me.y - h * s.RT;
-  const int row0 = rt * a.tile_rows;
-  const int nrows = (int)min((long long)a.tile_rows, (long long)s.T * a.G - row0);
+  const int4 me = a.meta[2 * c];                          // last CTA, rows, first token, key head
+  const int row0 = a.meta[2 * c + 1].x;
   const int r = blockIdx.y * 8 + warp_id();
-  if (r >= nrows) return;
-  const int n = me.z - c + 1;                             // parts: this CTA's and those of c + 1 .. me.z
+  if (me.x < 0 || r >= me.y) return;
+  const int n = me.x - c + 1;                             // parts: this CTA's and those of c + 1 .. me.x
   float m = -INFINITY;
   for (int i = lane; i < n; i += 32) {
     const long long slot = i == 0 ? 2LL * c + 1 : 2LL * (c + i);
@@ -664,8 +715,8 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
-  const long long tk = s.cu0 + t;
-  const int hq = h * a.G + g;
+  const long long tk = me.z + t;
+  const int hq = me.w * a.G + g;
   if (lane == 0) a.lse[tk * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2f;
   uint32_t* op = reinterpret_cast<uint32_t*>(a.o + tk * a.o_tok + hq * a.o_head + lane * kV);
 #pragma unroll
@@ -721,7 +772,7 @@ TreeLayout tree_layout(int rows, int d) {
   TreeLayout w;
   w.part_ml = up((size_t)kTreeCtas * 2 * rows * d * 4);
   w.meta = w.part_ml + up((size_t)kTreeCtas * 2 * rows * 8);
-  w.total = w.meta + up((size_t)kTreeCtas * sizeof(int4));
+  w.total = w.meta + up((size_t)kTreeCtas * 2 * sizeof(int4));
   return w;
 }
 
@@ -794,6 +845,7 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   const bool big = unit > 32;
   a.tile_rows = big ? kBigRows : unit <= 16 ? 16 : 32;
   a.slot_rows = min(a.tile_rows, most_rows(x.total, G));
+  a.chunk_shift = !big && x.cache.d * (fp8 ? 1 : 2) <= 128 ? 8 : 7;   // 32-key steps: SmallCfg
 
   CUtensorMap tk, tv;
   const long long rows = (long long)x.cache.pages * x.cache.Hk * x.cache.page_size;
@@ -801,7 +853,7 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
       !encode_cache(&tv, x.cache.v, rows, x.cache.d, fp8 ? 1 : 2, big ? x.cache.page_size : 16, !big))
     return FA_ERR_CUDA;
   // One CTA per SM, fewer where the longest possible sequences have fewer chunks.
-  const long long kt = ((long long)x.cache.max_pages * x.cache.page_size + kChunk - 1) / kChunk;
+  const long long kt = (((long long)x.cache.max_pages * x.cache.page_size - 1) >> a.chunk_shift) + 1;
   const long long rt = ((long long)x.max_new * G + a.tile_rows - 1) / a.tile_rows;
   long long most = kt * rt;
   most = most > kTreeCtas ? kTreeCtas : most * x.cache.Hk;

@@ -405,7 +405,7 @@ __global__ void __launch_bounds__(512, 1)
   }
   const long long total = total_chunks(a, blockIdx.x == 0 && warp == 0);
   const Part part = part_of(total, blockIdx.x, gridDim.x);
-  if (threadIdx.x == 0) a.meta[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  if (threadIdx.x == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   Cursor cur{};
   if (part.n > 0) cur = locate(a, part.lo);
   tc_fence_before();
@@ -761,8 +761,10 @@ __global__ void __launch_bounds__(512, 1)
       tc_fence_after();
       const bool whole = e.from_start && e.to_end;
       const int slot = 2 * blockIdx.x + (e.from_start ? 1 : 0);
-      if (q == 0 && rl == 0 && e.from_start && !e.to_end)
-        a.meta[blockIdx.x] = make_int4(e.b, e.unit, owner_cta(total, e.g + e.s.KT - 1, gridDim.x), 0);
+      if (q == 0 && rl == 0 && e.from_start && !e.to_end) {
+        a.meta[2 * blockIdx.x] = make_int4(owner_cta(total, e.g + e.s.KT - 1, gridDim.x), e.nrows, e.s.cu0, e.h);
+        a.meta[2 * blockIdx.x + 1] = make_int4(e.row0, 0, 0, 0);
+      }
       const bool odd = e.nu > 0 && *reinterpret_cast<volatile int*>(&sh.odd[q][(nseg - 1) & 7]) == nseg;
       const float inv = whole ? (l == 0.f ? 0.f : vref / l) : vref;
       const int hq = e.h * a.G + (R - t * a.G);
