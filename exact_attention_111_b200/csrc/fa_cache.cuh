@@ -153,7 +153,7 @@ __device__ __forceinline__ SeqView load_seq(const TreeArgs& a, int b, bool flag)
   s.T = (int)T;
   s.len = len;
   s.cu0 = c0;
-  s.RT = (int)(((long long)s.T * a.G + a.tile_rows - 1) / a.tile_rows);
+  s.RT = s.T * a.G <= a.tile_rows ? 1 : (s.T * a.G - 1) / a.tile_rows + 1;     // max_new * G < 2^31
   s.KT = (int)((L - 1) >> a.chunk_shift) + 1;
   return s;
 }
@@ -167,77 +167,86 @@ struct Cursor {
 };
 
 __device__ __forceinline__ void enter_unit(const TreeArgs& a, Cursor& c) {
-  c.h = c.u / c.s.RT;
+  c.h = c.s.RT == 1 ? c.u : c.u / c.s.RT;
   c.last = c.s.len + c.s.T - 1;
-  if (a.mask == nullptr) {       // chain: up to the row tile's last token
+  if (a.mask == nullptr && c.s.RT > 1) {   // chain: up to the row tile's last token
     const long long end = ((long long)(c.u - c.h * c.s.RT + 1) * a.tile_rows + a.G - 1) / a.G;
     if (end < c.s.T) c.last = c.s.len + (int)end - 1;
   }
 }
 
-// CTA cta's part of the line: n chunks from lo.  No part is empty while another has two.
-struct Part {
-  long long lo;
-  int n;
+// The line's total and equal parts: the first `more` CTAs take each + 1 chunks, the others `each`; no part
+// is empty while another has two.  Units of fewer than 2^31 chunks in all (32-bit divisions).
+struct Line {
+  int each, more;
+  __device__ __forceinline__ int count(int cta) const { return each + (cta < more ? 1 : 0); }
+  __device__ __forceinline__ int first(int cta) const { return cta * each + min(cta, more); }
+  // the CTA whose part holds chunk g
+  __device__ __forceinline__ int owner(int g) const {
+    const int cut = more * (each + 1);
+    return g < cut ? g / (each + 1) : more + (g - cut) / each;
+  }
 };
-__device__ __forceinline__ Part part_of(long long total, int cta, int ctas) {
-  const long long C = min((long long)ctas, total);
-  if (cta >= C) return Part{0, 0};
-  const long long lo = total * cta / C, hi = total * (cta + 1) / C;
-  return Part{lo, (int)(hi - lo)};
-}
-// The CTA whose part holds chunk g.
-__device__ __forceinline__ int owner_cta(long long total, long long g, int ctas) {
-  const long long C = min((long long)ctas, total);
-  return (int)(((g + 1) * C - 1) / total);
-}
 
-// Total chunks (every lane of a warp gets it).
-__device__ __forceinline__ long long total_chunks(const TreeArgs& a, bool flag) {
-  const int lane = threadIdx.x & 31;
-  long long n = 0;
-  for (int b = lane; b < a.c.B; b += 32) {
-    const SeqView s = load_seq(a, b, flag);
-    n += (long long)s.RT * s.KT * a.c.Hk;
+// This CTA's part and the place of its first chunk; one warp together.  flag: report sequences whose
+// lengths cannot be.
+struct Part {
+  Line line;
+  int lo, n;
+  Cursor at;
+};
+
+__device__ __forceinline__ Part find_part(const TreeArgs& a, bool flag) {
+  const int lane = threadIdx.x & 31, B = a.c.B;
+  // chunks of each lane's sequence of the first 32, and of all
+  SeqView s{0, 0, 0, 0, 0};
+  if (lane < B) s = load_seq(a, lane, flag);
+  long long n = (long long)s.RT * s.KT * a.c.Hk, total = n;
+  for (int b = 32 + lane; b < B; b += 32) {
+    const SeqView t = load_seq(a, b, flag);
+    total += (long long)t.RT * t.KT * a.c.Hk;
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n;
-}
-
-// The place of chunk g (below the total); one warp together.
-__device__ __forceinline__ Cursor locate(const TreeArgs& a, long long g) {
-  const int lane = threadIdx.x & 31;
-  Cursor c{};
-  for (int base = 0; base < a.c.B; base += 32) {
-    SeqView s{0, 0, 0, 0, 0};
-    if (base + lane < a.c.B) s = load_seq(a, base + lane, false);
-    const long long n = (long long)s.RT * s.KT * a.c.Hk;
-    long long inc = n;
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  Part p{};
+  if (total >= (1LL << 31)) {
+    if (flag) flag_range(a.c);
+    total = 0;
+  }
+  p.line.each = (int)total / (int)gridDim.x;
+  p.line.more = (int)total - p.line.each * (int)gridDim.x;
+  p.n = p.line.count(blockIdx.x);
+  p.lo = p.line.first(blockIdx.x);
+  if (p.n == 0) return p;
+  int g = p.lo;
+  for (int base = 0;;) {
+    int inc = (int)n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const long long t = __shfl_up_sync(0xffffffffu, inc, o);
+      const int t = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += t;
     }
     const unsigned hit = __ballot_sync(0xffffffffu, inc > g);
     if (hit != 0) {
       const int src = __ffs(hit) - 1;
-      const long long before = __shfl_sync(0xffffffffu, inc - n, src);
-      c.b = base + src;
-      c.s.T = __shfl_sync(0xffffffffu, s.T, src);
-      c.s.len = __shfl_sync(0xffffffffu, s.len, src);
-      c.s.cu0 = __shfl_sync(0xffffffffu, s.cu0, src);
-      c.s.RT = __shfl_sync(0xffffffffu, s.RT, src);
-      c.s.KT = __shfl_sync(0xffffffffu, s.KT, src);
-      const long long r = g - before;
-      c.u = (int)(r / c.s.KT);
-      c.kt = (int)(r - (long long)c.u * c.s.KT);
-      enter_unit(a, c);
-      return c;
+      g -= __shfl_sync(0xffffffffu, inc - (int)n, src);
+      p.at.b = base + src;
+      p.at.s.T = __shfl_sync(0xffffffffu, s.T, src);
+      p.at.s.len = __shfl_sync(0xffffffffu, s.len, src);
+      p.at.s.cu0 = __shfl_sync(0xffffffffu, s.cu0, src);
+      p.at.s.RT = __shfl_sync(0xffffffffu, s.RT, src);
+      p.at.s.KT = __shfl_sync(0xffffffffu, s.KT, src);
+      p.at.u = g / p.at.s.KT;
+      p.at.kt = g - p.at.u * p.at.s.KT;
+      enter_unit(a, p.at);
+      return p;
     }
     g -= __shfl_sync(0xffffffffu, inc, 31);
+    base += 32;
+    s = SeqView{0, 0, 0, 0, 0};
+    if (base + lane < B) s = load_seq(a, base + lane, false);
+    n = (long long)s.RT * s.KT * a.c.Hk;
   }
-  return c;
 }
 
 // The next chunk; only called while chunks are left.
@@ -251,6 +260,29 @@ __device__ __forceinline__ void next_unit(const TreeArgs& a, Cursor& c) {
     } while (c.s.T == 0);
   }
   enter_unit(a, c);
+}
+
+// Bits of the 32 keys from new token n0 on (negative: prefix) that token t of the sequence sees.
+__device__ __forceinline__ uint32_t visible32(const TreeArgs& a, const SeqView& s, int t, int n0) {
+  if (n0 <= -32) return 0xFFFFFFFFu;
+  if (n0 >= s.T) return 0u;
+  uint32_t v;
+  if (a.mask == nullptr) {
+    const int k = t + 1 - n0;
+    v = k >= 32 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << k) - 1u;
+  } else {
+    const unsigned long long* row = a.mask + (long long)(s.cu0 + t) * a.words;
+    if (n0 < 0) {
+      v = (uint32_t)(row[0] << -n0) | ((1u << -n0) - 1u);
+    } else {
+      const int w = n0 >> 6, sh = n0 & 63;
+      unsigned long long x = w < a.words ? row[w] >> sh : 0ull;
+      if (sh > 32 && w + 1 < a.words) x |= row[w + 1] << (64 - sh);
+      v = (uint32_t)x;
+    }
+  }
+  const int k = s.T - n0;        // new tokens end here
+  return k < 32 ? v & ((1u << k) - 1u) : v;
 }
 
 // Host side (fa_cache.cu): checks of the cache argument, and its view.

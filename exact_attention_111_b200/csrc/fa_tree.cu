@@ -49,6 +49,25 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// Whether one of the E4M3 codes or 16-bit floats of w is not finite.
+template <bool kFp8, bool kFp16>
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  if constexpr (kFp8) {
+    return (((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) != 0u;      // 0x7F + 1 carries into bit 7
+  } else {
+    constexpr uint32_t e = kFp16 ? 0x7C00u : 0x7F80u;
+    return (w & e) == e || ((w >> 16) & e) == e;
+  }
+}
+
+// Asynchronous copy of n <= 4 bytes (the rest of the four zeros), and its arrival on a barrier.
+__device__ __forceinline__ void copy4(void* dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Bytes (i, j) of w, E4M3 codes, as two fp16.
 template <int i, int j>
 __device__ __forceinline__ uint32_t expand2(uint32_t w) {
@@ -64,15 +83,19 @@ struct SmallCfg {
   // max and rescale) is then spent on 8 KB as with 16 rows of 256 bytes.
   static constexpr int kKeys = D * kEsz <= 128 ? 32 : 16;
   static constexpr int kChunkKeys = 8 * kKeys;           // a chunk: one step of each warp
-  static constexpr int kBoxes = kKeys / 16;              // copies of 16 rows (a page holds at least 16)
-  static constexpr int kBox = 16 * D * kEsz;
-  static constexpr int kHalf = kBoxes * kBox;            // K (or V) of a step
+  static constexpr int kHalf = kKeys * D * kEsz;         // K (or V) of a step
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = 24576 / kStage;
+  static constexpr int kStages = kFp8 && D == 128 ? 2 : 24576 / kStage;
   static constexpr int kRing = 8 * kStages * kStage;     // all warps
-  static constexpr int kSlot = 16 * (D / 2) * 4 + 144;   // half of one warp's O, its m, l and E, of 16 rows
-  static constexpr int kScales = kFp8 ? 8 * kStages * 2 * kKeys : 0;
-  static constexpr int kSmem = kRing + 4 * kSlot + kScales;
+  // Merge of the eight warps, eight rows at a time: each warp's O rows (8 floats apart beyond D: the
+  // fragments' stores then hit all banks), m and l of its rows, and E.
+  static constexpr int kRowF = D + 8;
+  static constexpr int kSlotF = 8 * kRowF;
+  static constexpr int kMerge = kRing, kStats = kMerge + 8 * kSlotF * 4, kBars = kStats + 8 * 16 * 4 + 8 * 4;
+  // E4M3: the steps' scale codes, K's then V's
+  static constexpr int kCodes = kBars + 8 * kStages * 8 + 16;
+  static constexpr int kSmem = kCodes + (kFp8 ? 8 * kStages * 2 * kKeys : 0);
+  static_assert(kSmem <= 227 * 1024, "shared memory");
   // bytes between 16-byte chunks' rows: 128-byte panels (64-byte rows for E4M3 at d = 64)
   static constexpr int kRowB = D * kEsz < 128 ? 64 : 128;
 };
@@ -80,17 +103,19 @@ struct SmallCfg {
 // Shared-memory offset of 16-byte chunk c of row r of K or V of a step as TMA wrote it.
 template <int D, bool kFp8>
 __device__ __forceinline__ uint32_t swz(int r, int c) {
-  const uint32_t box = (r >> 4) * SmallCfg<D, kFp8>::kBox;
-  if constexpr (SmallCfg<D, kFp8>::kRowB == 64) return box + (r & 15) * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  else return box + (c >> 3) * 2048 + (r & 15) * 128 + (((c & 7) ^ (r & 7)) << 4);
+  // (two panels only with 16 keys, one copy)
+  if constexpr (SmallCfg<D, kFp8>::kRowB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+  else return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // kFp16: type of q and o.  A 16-bit cache's products are in that type.  An E4M3 cache's are in fp16, which
 // holds every code exactly: K's scale multiplies the score (32 bits), V's the probability before it
 // is rounded, p * 2^(e - E) with E a warp's own reference: 2^8 under the scales of its first keys,
-// moved (and O with it) when a scale is 2^15 above it.  So p * 2^(e - E) has fp16's full eleven
-// bits down to 2^-22 for keys of the usual scale, three more than bf16.  bf16 queries enter as fp16 with a
-// power of two for each row (row_factor).
+// moved (and O with it) when a scale is 2^11 above it.  So p * 2^(e - E) has fp16's full eleven
+// bits down to 2^-22 for keys of the usual scale, three more than bf16; and the running max may lag
+// by 2^4 before O is rescaled (p <= 2^4, p * 2^(e - E) <= 2^15): with few steps in a segment some
+// row's max grows in almost every one.  bf16 queries enter as fp16 with a power of two for each row
+// (row_factor).
 template <int D, bool kFp8, bool kFp16, int kMT>
 __global__ void __launch_bounds__(256, 1)
     tree_small_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -101,39 +126,36 @@ __global__ void __launch_bounds__(256, 1)
   constexpr int kG = C::kKeys / 16;                       // 16-key groups
   constexpr bool kMma16 = kFp8 || kFp16;                  // products in fp16
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  __shared__ uint64_t full[8][C::kStages];
-  __shared__ int abort_flag;
   if ((smem_addr(smem_raw) & 1023u) != 0) {               // the copies' swizzle needs it
     if (threadIdx.x == 0) atomicCAS(a.c.status, 0, kDevBadState);
     return;
   }
   const int warp = warp_id(), lane = lane_id();
   uint8_t* ring = smem_raw + warp * C::kStages * C::kStage;
-  uint8_t* slots = smem_raw + C::kRing;
-  uint8_t* scales = slots + 4 * C::kSlot + warp * C::kStages * 2 * C::kKeys;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + C::kBars) + warp * C::kStages;
+  volatile int* abort_flag = reinterpret_cast<int*>(smem_raw + C::kBars + 8 * C::kStages * 8);
+  uint8_t* codes = smem_raw + C::kCodes + warp * C::kStages * 2 * C::kKeys;
   const DevStatus st{a.c.status, a.timeout_ns};
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0)
-    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[warp][i], 1);
+    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], kFp8 ? 33 : 1);
   if (threadIdx.x == 0) {
-    abort_flag = 0;
+    *abort_flag = 0;
     prefetch_tmap(&tm_k);
     prefetch_tmap(&tm_v);
+    a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
   fence_barrier_init();
-
-  const long long total = total_chunks(a, blockIdx.x == 0 && warp == 0);
-  const Part part = part_of(total, blockIdx.x, gridDim.x);
-  if (threadIdx.x == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
+  const Part part = find_part(a, blockIdx.x == 0 && warp == 0);
   if (part.n == 0) return;
-  Cursor rd = locate(a, part.lo), ld = rd;
+  Cursor rd = part.at, ld = rd;
   int rd_left = part.n, ld_left = part.n;
   __syncthreads();
 
   // ---------------------------------------------------------------- loads
   // A step is loaded when its first key exists and some row of the tile may see it.  `ld` stands at
-  // the next step to load, whose page ids (lane i: box i) are on their way since the last.
+  // the next step to load; lane i's page id for its key p0 + i is on its way since the last.
   auto wanted = [&](const Cursor& c) { return c.kt * C::kChunkKeys + warp * C::kKeys <= c.last; };
   int page = 0;
   auto advance = [&](Cursor& c, int& left) {
@@ -143,50 +165,54 @@ __global__ void __launch_bounds__(256, 1)
   };
   auto look_up = [&]() {
     while (ld_left > 0 && !wanted(ld)) advance(ld, ld_left);
-    if (ld_left > 0 && lane < C::kBoxes) {
-      const int pos = ld.kt * C::kChunkKeys + warp * C::kKeys + 16 * lane;
+    if (ld_left > 0) {
+      const int pos = ld.kt * C::kChunkKeys + warp * C::kKeys + (lane & (C::kKeys - 1));
       if (pos < ld.s.len + ld.s.T) page = a.c.table[(long long)ld.b * a.c.table_stride + (pos >> a.c.page_shift)];
     }
   };
   int fs = 0;                                             // stage to fill
-  auto fill = [&]() {                                     // start the next wanted step's copies, if any
-    if (ld_left <= 0) return;
-    const int p0 = ld.kt * C::kChunkKeys + warp * C::kKeys, end = ld.s.len + ld.s.T;
-    uint64_t* bar = &full[warp][fs];
-    if (lane == 0) {
-      const int boxes = min(C::kBoxes, (end - p0 + 15) >> 4);     // that hold keys: scales come with them
-      mbar_arrive_expect_tx(bar, C::kStage + (kFp8 ? boxes * 32 : 0));
-    }
-    __syncwarp();
-    if (lane < C::kBoxes) {
-      const int pos = p0 + 16 * lane;
-      int row;
-      if (pos >= end) {                                   // past the end: a row behind the tensor reads as zeros
-        row = (a.c.pages * a.c.Hk) << a.c.page_shift;
-      } else {
-        if ((unsigned)page >= (unsigned)a.c.pages) {
-          flag_range(a.c);
-          page = 0;                                       // stay inside the cache
-        }
-        row = ((page * a.c.Hk + ld.h) << a.c.page_shift) + (pos & ((1 << a.c.page_shift) - 1));
+  auto fill = [&]() {                                     // start the copies of the step `ld` stands at
+    const int pos = ld.kt * C::kChunkKeys + warp * C::kKeys + (lane & (C::kKeys - 1));
+    const bool key = pos < ld.s.len + ld.s.T;
+    int row = (a.c.pages * a.c.Hk) << a.c.page_shift;     // past the end: a row behind the tensor reads as zeros
+    if (key) {
+      if ((unsigned)page >= (unsigned)a.c.pages) {
+        flag_range(a.c);
+        page = 0;                                         // stay inside the cache
       }
-      uint8_t* dst = ring + fs * C::kStage + lane * C::kBox;
+      row = ((page * a.c.Hk + ld.h) << a.c.page_shift) + (pos & ((1 << a.c.page_shift) - 1));
+    }
+    const int row2 = C::kKeys == 32 ? __shfl_sync(0xffffffffu, row, 16) : 0;
+    uint64_t* bar = &full[fs];
+    if (lane == 0) {
+      uint8_t* dst = ring + fs * C::kStage;
+      mbar_arrive_expect_tx(bar, C::kStage);
       tma_load_3d(dst, &tm_k, bar, 0, row, 0);
       tma_load_3d(dst + C::kHalf, &tm_v, bar, 0, row, 0);
-      if constexpr (kFp8) {
-        if (pos < end) {
-          bulk_load(scales + fs * 2 * C::kKeys + 16 * lane, a.c.ks + row, 16, bar);
-          bulk_load(scales + (fs * 2 + 1) * C::kKeys + 16 * lane, a.c.vs + row, 16, bar);
-        }
+      if (C::kKeys == 32 && a.c.page_shift == 4) {        // boxes of 16 rows: two
+        tma_load_3d(dst + C::kHalf / 2, &tm_k, bar, 0, row2, 0);
+        tma_load_3d(dst + C::kHalf + C::kHalf / 2, &tm_v, bar, 0, row2, 0);
       }
     }
+    if constexpr (kFp8) {
+      // scale codes, four keys a lane and set (zeros past the end); the barrier counts the lanes too
+      if ((lane & 3) == 0) {
+        const int left = ld.s.len + ld.s.T - pos;         // keys from this one on
+        const uint32_t n = left >= 4 ? 4 : left <= 0 ? 0 : left;
+        const int src = n > 0 ? row : 0;
+        copy4(codes + fs * 2 * C::kKeys + lane, a.c.ks + src, n);
+        copy4(codes + (fs * 2 + 1) * C::kKeys + lane, a.c.vs + src, n);
+      }
+      copy_arrive(bar);
+    }
+    __syncwarp();
     fs = fs + 1 == C::kStages ? 0 : fs + 1;
     advance(ld, ld_left);
     look_up();
   };
   look_up();
   int issued = 0;
-  for (int i = 0; i < C::kStages && ld_left > 0; ++i, ++issued) fill();
+  for (; issued < C::kStages && ld_left > 0; ++issued) fill();
 
   // ---------------------------------------------------------------- segments
   const int r0 = lane >> 2, tq = lane & 3;                // fragment row and column quad
@@ -196,9 +222,9 @@ __global__ void __launch_bounds__(256, 1)
     const SeqView s = rd.s;
     const int h = rd.h;
     const int row0 = (rd.u - h * s.RT) * a.tile_rows;
-    const int nrows = (int)min((long long)a.tile_rows, (long long)s.T * a.G - row0);
+    const int nrows = min(a.tile_rows, s.T * a.G - row0);
     const bool from_start = rd.kt == 0;
-    const long long seg_g = part.lo + (part.n - rd_left);  // the segment's first chunk in the line
+    const int seg_g = part.lo + (part.n - rd_left);       // the segment's first chunk in the line
 
     // Q fragments; rows past the unit's last read the last one (never stored)
     uint32_t qf[kMT][D / 16][4];
@@ -263,11 +289,11 @@ __global__ void __launch_bounds__(256, 1)
 
     // ------------------------------------------------------------ the segment's steps
     // Unit, sequence and head stay; only kt moves until the unit or the part ends.
-    const int kt_end = (int)min((long long)s.KT, (long long)rd.kt + rd_left);
+    const int kt_end = min(s.KT, rd.kt + min(rd_left, s.KT));
     for (int kt = rd.kt; kt < kt_end; ++kt) {
       const int p0 = kt * C::kChunkKeys + warp * C::kKeys;
       if (p0 > rd.last) continue;
-      if (ok) ok = mbar_wait(&full[warp][us], uphase, &abort_flag, st);
+      if (ok) ok = mbar_wait(&full[us], uphase, abort_flag, st);
       ok = __all_sync(0xffffffffu, ok);
       if (ok) {
         const uint8_t* sk = ring + us * C::kStage;
@@ -284,7 +310,6 @@ __global__ void __launch_bounds__(256, 1)
             for (int i = 0; i < 4; ++i) sc[mt][j][i] = 0.f;
         float kf[kST][2], vf[kST][2];
         if constexpr (kFp8) {
-          const uint8_t* sp = scales + us * 2 * C::kKeys;
 #pragma unroll
           for (int c = 0; c < D / 16; c += 2)
 #pragma unroll
@@ -302,10 +327,11 @@ __global__ void __launch_bounds__(256, 1)
                 }
               }
             }
-          // the largest of V's scales among the keys that exist
-          const uint32_t top = __reduce_max_sync(0xffffffffu, lane < min(C::kKeys, end) ? sp[C::kKeys + (lane & (C::kKeys - 1))] : 0u);
-          if ((int)top > eref + 15) {
-            const int e = (int)top - 8;
+          // the largest of V's scales (0 where no key is)
+          const int ck = codes[us * 2 * C::kKeys + lane], cv = codes[(us * 2 + 1) * C::kKeys + lane];
+          const int top = (int)__reduce_max_sync(0xffffffffu, (unsigned)cv);
+          if (top > eref + 11) {
+            const int e = top - 8;
             if (eref != kNoScale) {                       // rare: a scale far above the ones before
               const float f = exp2f((float)(eref - e));
 #pragma unroll
@@ -317,15 +343,14 @@ __global__ void __launch_bounds__(256, 1)
             }
             eref = e;
           }
+          const float fk = scale_value(ck), fv = scale_value(max(cv + 127 - eref, 0));
 #pragma unroll
-          for (int j = 0; j < kST; ++j) {
-            const int wk = *reinterpret_cast<const uint16_t*>(sp + 8 * j + 2 * tq);
-            const int wv = *reinterpret_cast<const uint16_t*>(sp + C::kKeys + 8 * j + 2 * tq);
-            kf[j][0] = scale_value(wk & 0xFF);
-            kf[j][1] = scale_value(wk >> 8);
-            vf[j][0] = scale_value(max((wv & 0xFF) + 127 - eref, 0));
-            vf[j][1] = scale_value(max((wv >> 8) + 127 - eref, 0));
-          }
+          for (int j = 0; j < kST; ++j)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              kf[j][i] = __shfl_sync(0xffffffffu, fk, 8 * j + 2 * tq + i);
+              vf[j][i] = __shfl_sync(0xffffffffu, fv, 8 * j + 2 * tq + i);
+            }
         } else {
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk)
@@ -342,42 +367,32 @@ __global__ void __launch_bounds__(256, 1)
         }
         // ---- scale, mask, online softmax
         uint32_t pf[kMT][kG][4];
-        unsigned see[kMT][2];                             // bit 2j + i: key 8j + 2 tq + i is visible
+        unsigned see[kMT][2];                             // bit 8j + i: key 8j + 2 tq + i is visible
 #pragma unroll
         for (int mt = 0; mt < kMT; ++mt) {
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             float x[kST][2];
-            see[mt][hf] = 0xFFu;
+            see[mt][hf] = 0xFFFFFFFFu;
 #pragma unroll
             for (int j = 0; j < kST; ++j)
 #pragma unroll
               for (int i = 0; i < 2; ++i) x[j][i] = sc[mt][j][2 * hf + i] * (kFp8 ? sl2[mt][hf] * kf[j][i] : sl2[mt][hf]);
             if (masked) {
-              const int t = tok[mt][hf];
+              see[mt][hf] = visible32(a, s, tok[mt][hf], p0 - s.len) >> (2 * tq);
 #pragma unroll
               for (int j = 0; j < kST; ++j)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  const int n = p0 + 8 * j + 2 * tq + i - s.len;     // new token of this key
-                  bool vis = n < 0;
-                  if (n >= 0 && n < s.T) {
-                    if (a.mask == nullptr) vis = n <= t;
-                    else vis = (n >> 6) < a.words &&
-                               ((a.mask[(long long)(s.cu0 + t) * a.words + (n >> 6)] >> (n & 63)) & 1);
-                  }
-                  if (!vis) {
-                    x[j][i] = -INFINITY;
-                    see[mt][hf] &= ~(1u << (2 * j + i));
-                  }
-                }
+                for (int i = 0; i < 2; ++i)
+                  if (!((see[mt][hf] >> (8 * j + i)) & 1u)) x[j][i] = -INFINITY;
             }
             float mx = fmaxf(x[0][0], x[0][1]);
 #pragma unroll
             for (int j = 1; j < kST; ++j) mx = max3f(mx, x[j][0], x[j][1]);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            const float mn = fmaxf(m[mt][hf], mx);
+            float mn = fmaxf(m[mt][hf], mx);
+            if (kFp8 && mn <= m[mt][hf] + 4.f) mn = m[mt][hf];    // (-inf stays -inf only when both are)
             const float neg = mn == -INFINITY ? 0.f : -mn;
             const float al = ex2(m[mt][hf] + neg);        // 0 while m = -inf
             m[mt][hf] = mn;
@@ -398,13 +413,12 @@ __global__ void __launch_bounds__(256, 1)
                 o[mt][n][2 * hf + 1] *= al;
               }
             }
-            // P to 16 bits, one rounding of at most half a step (the row sum keeps 32 bits); a
-            // masked key's scale may be anything, so its zero is not multiplied
+            // P to 16 bits, one rounding of at most half a step (the row sum keeps 32 bits)
 #pragma unroll
             for (int j = 0; j < kST; ++j) {
               if constexpr (kFp8) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) p[j][i] = masked && !((see[mt][hf] >> (2 * j + i)) & 1) ? 0.f : p[j][i] * vf[j][i];
+                p[j][0] *= vf[j][0];
+                p[j][1] *= vf[j][1];
               }
               pf[mt][j >> 1][hf + 2 * (j & 1)] = pack2<kMma16>(p[j][0], p[j][1]);
             }
@@ -435,20 +449,15 @@ __global__ void __launch_bounds__(256, 1)
         // whose values are not all finite makes its products one by one, visible keys only.
         bool apart = false;
         if (masked) {
+          // V's rows that exist, 16 bytes at a time over the warp
+          constexpr int kC = D * C::kEsz / 16;            // chunks of a row
           bool bad = false;
 #pragma unroll 1
-          for (int c = 0; c < kNT / kVT; ++c)
-#pragma unroll
-            for (int g = 0; g < kG; ++g) {
-              uint32_t b[kVT][2];
-              vfrag(g, c, b);
-#pragma unroll
-              for (int i = 0; i < 2 * kVT; ++i) {
-                const uint32_t w = b[i >> 1][i & 1] & keep(g, i & 1);
-                const uint32_t e = kMma16 ? 0x7C00u : 0x7F80u;
-                bad |= (w & e) == e || ((w >> 16) & e) == e;
-              }
-            }
+          for (int i = lane; i < min(C::kKeys, end) * kC; i += 32) {
+            const uint4 x = *reinterpret_cast<const uint4*>(sk + C::kHalf + swz<D, kFp8>(i / kC, i % kC));
+            bad |= not_finite<kFp8, kFp16>(x.x) || not_finite<kFp8, kFp16>(x.y) || not_finite<kFp8, kFp16>(x.z) ||
+                   not_finite<kFp8, kFp16>(x.w);
+          }
           apart = __any_sync(0xffffffffu, bad);
         }
         if (apart) {
@@ -467,7 +476,7 @@ __global__ void __launch_bounds__(256, 1)
                   if (j == k) pw = pf[mt][k >> 1][hf + 2 * (k & 1)];
                 const float2 f = unpack2<kMma16>(__shfl_sync(0xffffffffu, pw, src));
                 w[mt][hf] = i ? f.y : f.x;
-                v[mt][hf] = (__shfl_sync(0xffffffffu, see[mt][hf], src) >> (2 * j + i)) & 1;
+                v[mt][hf] = (__shfl_sync(0xffffffffu, see[mt][hf], src) >> (8 * j + i)) & 1;
               }
 #pragma unroll
             for (int n = 0; n < kNT; ++n)
@@ -519,200 +528,155 @@ __global__ void __launch_bounds__(256, 1)
     const bool to_end = kt_end == s.KT;
     rd_left -= kt_end - rd.kt;
 
-    // ------------------------------------------------------------ merge of the eight warps
+    // ------------------------------------------------------------ merge of the eight warps, results
+    // Eight rows at a time: every warp leaves its O, m, l (and E) in shared memory, then warp w sums
+    // row w.  A whole unit is normalised and stored; a cut one leaves its sums to the merge kernel:
+    // slot 0 of this CTA for a segment that began in an earlier CTA, slot 1 for one that only
+    // begins here.
+    const bool whole = from_start && to_end;
+    const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
+    if (threadIdx.x == 0 && from_start && !to_end) {
+      a.meta[2 * blockIdx.x] = make_int4(part.line.owner(seg_g + s.KT - 1), nrows, s.cu0, h);
+      a.meta[2 * blockIdx.x + 1] = make_int4(row0, 0, 0, 0);
+    }
+    float* so = reinterpret_cast<float*>(smem_raw + C::kMerge) + warp * C::kSlotF;
+    float* stats = reinterpret_cast<float*>(smem_raw + C::kStats);       // [warp][m of 8 rows, l of 8 rows]
+    int* es = reinterpret_cast<int*>(stats + 8 * 16);
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
+    for (int mt = 0; mt < kMT; ++mt)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
+        const int rb = mt * 16 + hf * 8;
+        if (rb >= nrows) continue;
         l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
         l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
-      }
-      int em = eref;                                      // E of this row block's O
-      for (int half = 4; half > 0; half >>= 1) {
-        float fa[2], fb[2];
+        if (rb > 0) __syncthreads();                      // the rows before are summed
+        if constexpr (kFp8) {
 #pragma unroll
-        for (int part2 = 0; part2 < 2; ++part2) {         // half of the columns at a time
-          constexpr int kH = kNT / 2;
-          __syncthreads();
-          if (warp >= half && warp < 2 * half) {
-            uint8_t* sl = slots + (warp - half) * C::kSlot;
-            float4* so = reinterpret_cast<float4*>(sl);
+          for (int c = 0; c < D / 16; ++c)
+            *reinterpret_cast<float4*>(so + r0 * C::kRowF + 16 * c + 4 * tq) =
+                make_float4(o[mt][2 * c][2 * hf], o[mt][2 * c + 1][2 * hf], o[mt][2 * c][2 * hf + 1],
+                            o[mt][2 * c + 1][2 * hf + 1]);
+        } else {
 #pragma unroll
-            for (int n = 0; n < kH; ++n) {
-              const float (&x)[4] = o[mt][part2 * kH + n];
-              so[n * 32 + lane] = make_float4(x[0], x[1], x[2], x[3]);
-            }
-            float* sm = reinterpret_cast<float*>(sl + 16 * (D / 2) * 4);
-            if (part2 == 0 && tq == 0) {
-              sm[r0] = m[mt][0];
-              sm[r0 + 8] = m[mt][1];
-              sm[16 + r0] = l[mt][0];
-              sm[24 + r0] = l[mt][1];
-            }
-            if (kFp8 && part2 == 0 && lane == 0) reinterpret_cast<int*>(sm)[32] = em;
-          }
-          __syncthreads();
-          if (warp < half) {
-            const uint8_t* sl = slots + warp * C::kSlot;
-            const float4* so = reinterpret_cast<const float4*>(sl);
-            if (part2 == 0) {
-              const float* sm = reinterpret_cast<const float*>(sl + 16 * (D / 2) * 4);
-              float ga = 1.f, gb = 1.f;                   // factors of O beside the maxima's
-              if constexpr (kFp8) {
-                const int eb = reinterpret_cast<const int*>(sm)[32], en = max(em, eb);
-                ga = exp2f((float)(em - en));
-                gb = exp2f((float)(eb - en));
-                em = en;
-              }
-#pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                const float mb = sm[r0 + 8 * hf], lb = sm[16 + r0 + 8 * hf];
-                const float mn = fmaxf(m[mt][hf], mb);
-                const float neg = mn == -INFINITY ? 0.f : -mn;
-                fa[hf] = ex2(m[mt][hf] + neg);
-                fb[hf] = ex2(mb + neg);
-                m[mt][hf] = mn;
-                l[mt][hf] = l[mt][hf] * fa[hf] + lb * fb[hf];
-                fa[hf] *= ga;
-                fb[hf] *= gb;
-              }
-            }
-#pragma unroll
-            for (int n = 0; n < kH; ++n) {
-              const float4 w = so[n * 32 + lane];
-              float (&x)[4] = o[mt][part2 * kH + n];
-              x[0] = x[0] * fa[0] + w.x * fb[0];
-              x[1] = x[1] * fa[0] + w.y * fb[0];
-              x[2] = x[2] * fa[1] + w.z * fb[1];
-              x[3] = x[3] * fa[1] + w.w * fb[1];
-            }
-          }
+          for (int n = 0; n < kNT; ++n)
+            *reinterpret_cast<float2*>(so + r0 * C::kRowF + 8 * n + 2 * tq) =
+                make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
         }
-      }
-      if (mt == kMT - 1) eref = em;
-    }
-
-    // ------------------------------------------------------------ results
-    // A whole unit is normalised and stored; a cut one leaves its sums to the merge: slot 0 of this
-    // CTA for a segment that began in an earlier CTA, slot 1 for one that only begins here.
-    if (warp == 0) {
-      const bool whole = from_start && to_end;
-      const int slot = 2 * blockIdx.x + (from_start ? 1 : 0);
-      if (lane == 0 && from_start && !to_end) {
-        a.meta[2 * blockIdx.x] = make_int4(owner_cta(total, seg_g + s.KT - 1, gridDim.x), nrows, s.cu0, h);
-        a.meta[2 * blockIdx.x + 1] = make_int4(row0, 0, 0, 0);
-      }
+        if (tq == 0) {
+          stats[warp * 16 + r0] = m[mt][hf];
+          stats[warp * 16 + 8 + r0] = l[mt][hf];
+        }
+        if (kFp8 && lane == 0) es[warp] = eref;
+        __syncthreads();
+        const int r = rb + warp;
+        if (r < nrows) {
+          constexpr int kV = D / 32;                      // columns of a lane
+          float mr = -INFINITY;
+          int er = kNoScale;
 #pragma unroll
-      for (int mt = 0; mt < kMT; ++mt)
+          for (int w = 0; w < 8; ++w) {
+            mr = fmaxf(mr, stats[w * 16 + warp]);
+            if constexpr (kFp8) er = max(er, es[w]);
+          }
+          const float neg = mr == -INFINITY ? 0.f : -mr;
+          float lr = 0.f, x[kV] = {};
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int r = mt * 16 + hf * 8 + r0;
-          if (r >= nrows) continue;
-          const float lv = l[mt][hf];
+          for (int w = 0; w < 8; ++w) {
+            float f = ex2(stats[w * 16 + warp] + neg);
+            lr += f * stats[w * 16 + 8 + warp];
+            if constexpr (kFp8) f *= exp2f((float)(es[w] - er));
+            const float* src = reinterpret_cast<const float*>(smem_raw + C::kMerge) + w * C::kSlotF + warp * C::kRowF + lane * kV;
+#pragma unroll
+            for (int i = 0; i < kV; i += 2) {
+              const float2 v = *reinterpret_cast<const float2*>(src + i);
+              x[i] += f * v.x;
+              x[i + 1] += f * v.y;
+            }
+          }
           // what O is a multiple of: 2^(E - 127)
-          const float vref = kFp8 && eref != kNoScale ? exp2f((float)(eref - 127)) : 1.f;
+          const float vref = kFp8 && er != kNoScale ? exp2f((float)(er - 127)) : 1.f;
           if (whole) {
-            const float inv = lv == 0.f ? 0.f : vref / lv;
+            const float inv = lr == 0.f ? 0.f : vref / lr;
             const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
             const long long tk = s.cu0 + t;
             const int hq = h * a.G + g;
-            if (tq == 0) a.lse[tk * a.Hq + hq] = lv == 0.f ? -INFINITY : (m[mt][hf] + log2f(lv)) * kLn2f;
-            uint16_t* op = a.o + tk * a.o_tok + hq * a.o_head;
-            if constexpr (kFp8) {
+            if (lane == 0) a.lse[tk * a.Hq + hq] = lr == 0.f ? -INFINITY : (mr + log2f(lr)) * kLn2f;
+            uint32_t* op = reinterpret_cast<uint32_t*>(a.o + tk * a.o_tok + hq * a.o_head + lane * kV);
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c)
-                *reinterpret_cast<uint2*>(op + 16 * c + 4 * tq) =
-                    make_uint2(pack2<kFp16>(o[mt][2 * c][2 * hf] * inv, o[mt][2 * c + 1][2 * hf] * inv),
-                               pack2<kFp16>(o[mt][2 * c][2 * hf + 1] * inv, o[mt][2 * c + 1][2 * hf + 1] * inv));
-            } else {
-#pragma unroll
-              for (int n = 0; n < kNT; ++n)
-                *reinterpret_cast<uint32_t*>(op + 8 * n + 2 * tq) =
-                    pack2<kFp16>(o[mt][n][2 * hf] * inv, o[mt][n][2 * hf + 1] * inv);
-            }
+            for (int i = 0; i < kV; i += 2) op[i / 2] = pack2<kFp16>(x[i] * inv, x[i + 1] * inv);
           } else {
-            float* pp = a.part_o + ((long long)slot * a.slot_rows + r) * D;
-            if (tq == 0) {
-              float* ml = a.part_ml + ((long long)slot * a.slot_rows + r) * 2;
-              ml[0] = m[mt][hf];
-              ml[1] = lv;
-            }
-            if constexpr (kFp8) {
+            const long long at = (long long)slot * a.slot_rows + r;
+            if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(mr, lr);
 #pragma unroll
-              for (int c = 0; c < D / 16; ++c)
-                *reinterpret_cast<float4*>(pp + 16 * c + 4 * tq) =
-                    make_float4(o[mt][2 * c][2 * hf] * vref, o[mt][2 * c + 1][2 * hf] * vref,
-                                o[mt][2 * c][2 * hf + 1] * vref, o[mt][2 * c + 1][2 * hf + 1] * vref);
-            } else {
-#pragma unroll
-              for (int n = 0; n < kNT; ++n)
-                *reinterpret_cast<float2*>(pp + 8 * n + 2 * tq) =
-                    make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
-            }
+            for (int i = 0; i < kV; i += 2)
+              *reinterpret_cast<float2*>(a.part_o + at * D + lane * kV + i) = make_float2(x[i] * vref, x[i + 1] * vref);
           }
         }
-    }
+      }
+    if (rd_left > 0) __syncthreads();                     // the last rows are summed
     if (rd_left > 0) next_unit(a, rd);
   }
   // A wait that ran out left copies in flight: let them land before the shared memory goes away.
   if (!ok && lane == 0)
     for (int i = max(used, issued - C::kStages); i < issued; ++i)
-      mbar_wait_drain(&full[warp][i % C::kStages], (i / C::kStages) & 1, st);
+      mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1, st);
 }
 
 // ------------------------------------------------------------------------------------
-// Merge of the units cut between CTAs: block (c, y) takes the unit that begins in CTA c and ends in
-// a later one, a warp one of its rows.  With parts (m_i, l_i, O_i):
+// Merge of the units cut between CTAs: block (c, y) takes rows of the unit that begins in CTA c and ends
+// in a later one.  With parts (m_i, l_i, O_i):
 //     O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i.
+// kSplit warps share a row's parts (few rows, up to 148 parts each) or each warp has its own row.
 // ------------------------------------------------------------------------------------
-template <int D, bool kFp16>
+template <int D, bool kFp16, int kSplit>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   constexpr int kV = D / 32;                              // columns per lane
+  __shared__ float so[kSplit > 1 ? 8 : 1][D];
+  __shared__ float sl[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int c = blockIdx.x, lane = lane_id();
+  const int c = blockIdx.x, lane = lane_id(), warp = warp_id();
   const int4 me = a.meta[2 * c];                          // last CTA, rows, first token, key head
   const int row0 = a.meta[2 * c + 1].x;
-  const int r = blockIdx.y * 8 + warp_id();
+  const int r = kSplit > 1 ? blockIdx.y : blockIdx.y * 8 + warp, sub = kSplit > 1 ? warp : 0;
   if (me.x < 0 || r >= me.y) return;
   const int n = me.x - c + 1;                             // parts: this CTA's and those of c + 1 .. me.x
+  auto at = [&](int i) { return (2LL * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r; };
   float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) {
-    const long long slot = i == 0 ? 2LL * c + 1 : 2LL * (c + i);
-    m = fmaxf(m, a.part_ml[(slot * a.slot_rows + r) * 2]);
-  }
+  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_ml[at(i) * 2]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float neg = m == -INFINITY ? 0.f : -m;
   float l = 0.f, acc[kV] = {};
-  for (int i0 = 0; i0 < n; i0 += 32) {
-    float w = 0.f;
-    if (i0 + lane < n) {
-      const long long slot = i0 + lane == 0 ? 2LL * c + 1 : 2LL * (c + i0 + lane);
-      const float* ml = a.part_ml + (slot * a.slot_rows + r) * 2;
-      w = ex2(ml[0] + neg);
-      l += w * ml[1];
-    }
-    const int k = min(32, n - i0);
-#pragma unroll 8
-    for (int i = 0; i < k; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const long long slot = i0 + i == 0 ? 2LL * c + 1 : 2LL * (c + i0 + i);
-      const float* p = a.part_o + (slot * a.slot_rows + r) * D + lane * kV;
-      if constexpr (kV == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(p);
-        acc[0] += wi * x.x;
-        acc[1] += wi * x.y;
-        acc[2] += wi * x.z;
-        acc[3] += wi * x.w;
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        acc[0] += wi * x.x;
-        acc[1] += wi * x.y;
-      }
+#pragma unroll 4
+  for (int i = sub; i < n; i += kSplit) {
+    const long long k = at(i);
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + k * 2);
+    const float w = ex2(ml.x + neg);
+    l += w * ml.y;
+#pragma unroll
+    for (int j = 0; j < kV; j += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(a.part_o + k * D + lane * kV + j);
+      acc[j] += w * x.x;
+      acc[j + 1] += w * x.y;
     }
   }
+  if constexpr (kSplit > 1) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    for (int j = 0; j < kV; ++j) so[warp][lane * kV + j] = acc[j];
+    if (lane == 0) sl[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int j = 0; j < kV; ++j) acc[j] = 0.f;
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      l += sl[w];
+#pragma unroll
+      for (int j = 0; j < kV; ++j) acc[j] += so[w][lane * kV + j];
+    }
+  }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
   const long long tk = me.z + t;
@@ -720,7 +684,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   if (lane == 0) a.lse[tk * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2f;
   uint32_t* op = reinterpret_cast<uint32_t*>(a.o + tk * a.o_tok + hq * a.o_head + lane * kV);
 #pragma unroll
-  for (int i = 0; i < kV; i += 2) op[i / 2] = pack2<kFp16>(acc[i] * inv, acc[i + 1] * inv);
+  for (int j = 0; j < kV; j += 2) op[j / 2] = pack2<kFp16>(acc[j] * inv, acc[j + 1] * inv);
 }
 
 template <int D, bool kFp8, bool kFp16, int kMT>
@@ -751,7 +715,8 @@ cudaError_t launch_small_d(const CUtensorMap& tk, const CUtensorMap& tv, const T
 template <int D, bool kFp16>
 cudaError_t launch_merge_d(const TreeArgs& a, int ctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(ctas, (a.tile_rows + 7) / 8, 1);
+  const bool few = a.slot_rows <= 32;
+  cfg.gridDim = dim3(ctas, few ? a.slot_rows : (a.slot_rows + 7) / 8, 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -759,7 +724,8 @@ cudaError_t launch_merge_d(const TreeArgs& a, int ctas, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kFp16>, a);
+  return few ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kFp16, 8>, a)
+             : cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kFp16, 1>, a);
 }
 
 struct TreeLayout {
@@ -848,9 +814,10 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   a.chunk_shift = !big && x.cache.d * (fp8 ? 1 : 2) <= 128 ? 8 : 7;   // 32-key steps: SmallCfg
 
   CUtensorMap tk, tv;
+  const int box = big || a.chunk_shift == 7 ? (big ? x.cache.page_size : 16) : min(x.cache.page_size, 32);   // rows of a copy
   const long long rows = (long long)x.cache.pages * x.cache.Hk * x.cache.page_size;
-  if (!encode_cache(&tk, x.cache.k, rows, x.cache.d, fp8 ? 1 : 2, big ? x.cache.page_size : 16, !big) ||
-      !encode_cache(&tv, x.cache.v, rows, x.cache.d, fp8 ? 1 : 2, big ? x.cache.page_size : 16, !big))
+  if (!encode_cache(&tk, x.cache.k, rows, x.cache.d, fp8 ? 1 : 2, box, !big) ||
+      !encode_cache(&tv, x.cache.v, rows, x.cache.d, fp8 ? 1 : 2, box, !big))
     return FA_ERR_CUDA;
   // One CTA per SM, fewer where the longest possible sequences have fewer chunks.
   const long long kt = (((long long)x.cache.max_pages * x.cache.page_size - 1) >> a.chunk_shift) + 1;

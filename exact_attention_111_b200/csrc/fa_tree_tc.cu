@@ -48,7 +48,7 @@ struct BigCfg {
 
 // A segment: the CTA's run of tiles [kt0, kt0 + n) of one unit; nu of them can be seen by some row.
 struct Seg {
-  long long g;                   // first chunk in the line
+  int g;                         // first chunk in the line
   SeqView s;
   int b, h, unit, row0, nrows, kt0, n, nu;
   bool from_start, to_end;
@@ -57,11 +57,10 @@ struct Seg {
 // A walk over the CTA's segments.
 struct Walk {
   Cursor c;
-  long long g;
-  int left;
+  int g, left;
   Seg e;
-  __device__ __forceinline__ void start(const Cursor& c0, const Part& p) {
-    c = c0;
+  __device__ __forceinline__ void start(const Part& p) {
+    c = p.at;
     g = p.lo;
     left = p.n;
   }
@@ -72,7 +71,7 @@ struct Walk {
     e.h = c.h;
     e.unit = c.u;
     e.row0 = (c.u - c.h * c.s.RT) * a.tile_rows;
-    e.nrows = (int)min((long long)a.tile_rows, (long long)c.s.T * a.G - e.row0);
+    e.nrows = min(a.tile_rows, c.s.T * a.G - e.row0);
     e.kt0 = c.kt;
     e.n = min(c.s.KT - c.kt, left);
     e.nu = max(0, min(e.n, c.last / kChunk + 1 - c.kt));
@@ -113,29 +112,6 @@ __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.al
 
 // Whether tile kt holds new tokens or reaches past them.
 __device__ __forceinline__ bool tail_tile(const Seg& e, int kt) { return (kt + 1) * kChunk > e.s.len; }
-
-// Bits of the 32 keys from new token n0 on (negative: prefix) that token t of the sequence sees.
-__device__ __forceinline__ uint32_t visible32(const TreeArgs& a, const SeqView& s, int t, int n0) {
-  if (n0 <= -32) return 0xFFFFFFFFu;
-  if (n0 >= s.T) return 0u;
-  uint32_t v;
-  if (a.mask == nullptr) {
-    const int k = t + 1 - n0;
-    v = k >= 32 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << k) - 1u;
-  } else {
-    const unsigned long long* row = a.mask + (long long)(s.cu0 + t) * a.words;
-    if (n0 < 0) {
-      v = (uint32_t)(row[0] << -n0) | ((1u << -n0) - 1u);
-    } else {
-      const int w = n0 >> 6, sh = n0 & 63;
-      unsigned long long x = w < a.words ? row[w] >> sh : 0ull;
-      if (sh > 32 && w + 1 < a.words) x |= row[w + 1] << (64 - sh);
-      v = (uint32_t)x;
-    }
-  }
-  const int k = s.T - n0;        // new tokens end here
-  return k < 32 ? v & ((1u << k) - 1u) : v;
-}
 
 // E4M3 rows enter the fp16 products as code * 2^(scale - E): a code is exact in fp16, and with E the
 // largest scale of the tile's keys what a row of a much smaller scale loses is below 2^-25 of the
@@ -403,11 +379,8 @@ __global__ void __launch_bounds__(512, 1)
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
-  const long long total = total_chunks(a, blockIdx.x == 0 && warp == 0);
-  const Part part = part_of(total, blockIdx.x, gridDim.x);
+  const Part part = find_part(a, blockIdx.x == 0 && warp == 0);
   if (threadIdx.x == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-  Cursor cur{};
-  if (part.n > 0) cur = locate(a, part.lo);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -416,7 +389,7 @@ __global__ void __launch_bounds__(512, 1)
   if (warp >= C::kLoadWarp) {
     reg_dec<C::kRegOther>();
     Walk w;
-    w.start(cur, part);
+    w.start(part);
     const Seg& e = w.e;
     if (kFp8 && warp == C::kLoadWarp) {
       stage_role<D>(a, sh, sC, &tm_k, &tm_v, w);
@@ -553,7 +526,7 @@ __global__ void __launch_bounds__(512, 1)
     int seg[2] = {0, 0};
     bool ok = true;
     Walk w;
-    w.start(cur, part);
+    w.start(part);
     const Seg& e = w.e;
     uint32_t eref = 0;
     while (ok && w.next(a)) {
@@ -656,7 +629,7 @@ __global__ void __launch_bounds__(512, 1)
     int tile = 0;                                         // tiles of the CTA before this segment
     bool ok = true;
     Walk& w = sh.walk[warp];
-    if (lane == 0) w.start(cur, part);
+    if (lane == 0) w.start(part);
     const Seg& e = w.e;
     while (ok) {
       __syncwarp();
@@ -762,7 +735,7 @@ __global__ void __launch_bounds__(512, 1)
       const bool whole = e.from_start && e.to_end;
       const int slot = 2 * blockIdx.x + (e.from_start ? 1 : 0);
       if (q == 0 && rl == 0 && e.from_start && !e.to_end) {
-        a.meta[2 * blockIdx.x] = make_int4(owner_cta(total, e.g + e.s.KT - 1, gridDim.x), e.nrows, e.s.cu0, e.h);
+        a.meta[2 * blockIdx.x] = make_int4(part.line.owner(e.g + e.s.KT - 1), e.nrows, e.s.cu0, e.h);
         a.meta[2 * blockIdx.x + 1] = make_int4(e.row0, 0, 0, 0);
       }
       const bool odd = e.nu > 0 && *reinterpret_cast<volatile int*>(&sh.odd[q][(nseg - 1) & 7]) == nseg;
