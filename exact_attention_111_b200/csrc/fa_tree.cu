@@ -10,9 +10,12 @@
 // read once and its bytes are the bound.  One CTA per SM, eight warps.  A chunk of 128 keys is
 // eight steps of 16 keys; warp w always takes step w, with a ring of its own that its lane 0 fills by
 // TMA several steps ahead, so warps never wait for one another inside a segment and loads cross
-// from one unit to the next without a pause.  Each warp keeps its own m, l and O (16 * kMT rows,
-// mma.sync m16n8k16 fragments in registers); at the end of a segment (the CTA's run of chunks of one
-// unit) the eight are merged through shared memory.
+// from one unit to the next without a pause.  Each warp keeps its own m, l and O; at the end of a
+// segment (the CTA's run of chunks of one unit) the eight are merged through shared memory.
+//
+// The products are made transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): keys and columns
+// fill the 16-wide side and rows come in eights, so four or eight query heads of a group cost
+// half of what a 16-row tile would, in products, exponentials and registers.
 #include <climits>
 #include <cmath>
 
@@ -34,6 +37,12 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// Transposes an 8 x 8 matrix of 16-bit values held as fragments (lane: row lane / 4, columns 2 (lane % 4) ..).
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
 }
 template <bool kFp16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -87,9 +96,9 @@ struct SmallCfg {
   static constexpr int kStage = 2 * kHalf;
   static constexpr int kStages = kFp8 && D == 128 ? 2 : 24576 / kStage;
   static constexpr int kRing = 8 * kStages * kStage;     // all warps
-  // Merge of the eight warps, eight rows at a time: each warp's O rows (8 floats apart beyond D: the
+  // Merge of the eight warps, eight rows at a time: each warp's O rows (4 floats apart beyond D: the
   // fragments' stores then hit all banks), m and l of its rows, and E.
-  static constexpr int kRowF = D + 8;
+  static constexpr int kRowF = D + 4;
   static constexpr int kSlotF = 8 * kRowF;
   static constexpr int kMerge = kRing, kStats = kMerge + 8 * kSlotF * 4, kBars = kStats + 8 * 16 * 4 + 8 * 4;
   // E4M3: the steps' scale codes, K's then V's
@@ -116,13 +125,11 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 // by 2^4 before O is rescaled (p <= 2^4, p * 2^(e - E) <= 2^15): with few steps in a segment some
 // row's max grows in almost every one.  bf16 queries enter as fp16 with a power of two for each row
 // (row_factor).
-template <int D, bool kFp8, bool kFp16, int kMT>
+template <int D, bool kFp8, bool kFp16, int kNR>
 __global__ void __launch_bounds__(256, 1)
     tree_small_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const TreeArgs a) {
   using C = SmallCfg<D, kFp8>;
-  constexpr int kNT = D / 8;                              // 8-column tiles of O
-  constexpr int kST = C::kKeys / 8;                       // 8-key tiles of S
   constexpr int kG = C::kKeys / 16;                       // 16-key groups
   constexpr bool kMma16 = kFp8 || kFp16;                  // products in fp16
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -226,64 +233,68 @@ __global__ void __launch_bounds__(256, 1)
     const bool from_start = rd.kt == 0;
     const int seg_g = part.lo + (part.n - rd_left);       // the segment's first chunk in the line
 
-    // Q fragments; rows past the unit's last read the last one (never stored)
-    uint32_t qf[kMT][D / 16][4];
-    int tok[kMT][2];
-    float sl2[kMT][2];                                    // score factors of the lane's rows
+    // Q fragments: lane / 4 is the row; rows past the unit's last read the last one (never stored).
+    // Results and row statistics: rows 2 tq and 2 tq + 1 of each eight.
+    uint32_t qf[kNR][D / 16][2];
+    int tok[kNR][2];
+    float sl2[kNR][2];                                    // score factors
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
+    for (int nr = 0; nr < kNR; ++nr) {
+      const int r = row0 + min(nr * 8 + r0, nrows - 1);
+      const int t = r / a.G, g = r - t * a.G;
+      const uint16_t* qp = a.q + (s.cu0 + t) * a.q_tok + (h * a.G + g) * a.q_head;
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int r = row0 + min(mt * 16 + hf * 8 + r0, nrows - 1);
-        const int t = r / a.G, g = r - t * a.G;
-        tok[mt][hf] = t;
-        const uint16_t* qp = a.q + (s.cu0 + t) * a.q_tok + (h * a.G + g) * a.q_head;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          if constexpr (kFp8) {
-            // the order of the 16 columns of a step is free as long as K's agrees: a lane's
-            // four E4M3 columns 4 tq .. 4 tq + 3 stand at places (2tq, 2tq+1, 2tq+8, 2tq+9)
-            const uint2 w = *reinterpret_cast<const uint2*>(qp + kk * 16 + 4 * tq);
-            qf[mt][kk][hf] = w.x;
-            qf[mt][kk][hf + 2] = w.y;
-          } else {
-            qf[mt][kk][hf] = *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 2 * tq);
-            qf[mt][kk][hf + 2] = *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 8 + 2 * tq);
-          }
-        }
-        sl2[mt][hf] = a.scale_log2;
-        if constexpr (kFp8 && !kFp16) {
-          float amax = 0.f;
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const float2 f = unpack2<false>(qf[mt][kk][hf + i]);
-              amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-          amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-          const int k = row_factor(amax);
-          const float f = scale_value(127 + k);
-          sl2[mt][hf] *= scale_value(127 - k);
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-              const float2 v = unpack2<false>(qf[mt][kk][hf + i]);
-              qf[mt][kk][hf + i] = pack2<true>(v.x * f, v.y * f);
-            }
+      for (int kk = 0; kk < D / 16; ++kk) {
+        if constexpr (kFp8) {
+          // the order of the 16 columns of a step is free as long as K's agrees: a lane's
+          // four E4M3 columns 4 tq .. 4 tq + 3 stand at places (2tq, 2tq+1, 2tq+8, 2tq+9)
+          const uint2 w = *reinterpret_cast<const uint2*>(qp + kk * 16 + 4 * tq);
+          qf[nr][kk][0] = w.x;
+          qf[nr][kk][1] = w.y;
+        } else {
+          qf[nr][kk][0] = *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 2 * tq);
+          qf[nr][kk][1] = *reinterpret_cast<const uint32_t*>(qp + kk * 16 + 8 + 2 * tq);
         }
       }
-    float o[kMT][kNT][4], m[kMT][2], l[kMT][2];
+      float f = a.scale_log2;
+      if constexpr (kFp8 && !kFp16) {
+        float amax = 0.f;
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt) {
+        for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-      for (int n = 0; n < kNT; ++n)
+          for (int i = 0; i < 2; ++i) {
+            const float2 v = unpack2<false>(qf[nr][kk][i]);
+            amax = fmaxf(amax, fmaxf(fabsf(v.x), fabsf(v.y)));
+          }
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+        const int k = row_factor(amax);
+        const float to = scale_value(127 + k);
+        f *= scale_value(127 - k);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[mt][n][i] = 0.f;
-      m[mt][0] = m[mt][1] = -INFINITY;
-      l[mt][0] = l[mt][1] = 0.f;
+        for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float2 v = unpack2<false>(qf[nr][kk][i]);
+            qf[nr][kk][i] = pack2<true>(v.x * to, v.y * to);
+          }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sl2[nr][e] = kFp8 && !kFp16 ? __shfl_sync(0xffffffffu, f, 4 * (2 * tq + e)) : f;
+        tok[nr][e] = __shfl_sync(0xffffffffu, t, 4 * (2 * tq + e));
+      }
+    }
+    // O^T: columns r0 and r0 + 8 (E4M3: 2 r0 and 2 r0 + 1) of each 16, rows 2 tq, 2 tq + 1
+    float o[kNR][D / 16][4], m[kNR][2], l[kNR][2];
+#pragma unroll
+    for (int nr = 0; nr < kNR; ++nr) {
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[nr][n][i] = 0.f;
+      m[nr][0] = m[nr][1] = -INFINITY;
+      l[nr][0] = l[nr][1] = 0.f;
     }
     int eref = kNoScale;                                  // E4M3: E (as a scale code) of what O holds
 
@@ -300,31 +311,29 @@ __global__ void __launch_bounds__(256, 1)
         const uint32_t ak = smem_addr(sk), av = ak + C::kHalf;
         const int end = s.len + s.T - p0;                 // keys of the step from here on do not exist
         const bool masked = p0 + C::kKeys > s.len;
-        // ---- S = Q K^T, 16 * kMT rows x kKeys keys
-        float sc[kMT][kST][4];
+        // ---- S^T = K Q^T, kKeys keys x 8 kNR rows: keys r0 and r0 + 8 of each 16, rows 2 tq, 2 tq + 1
+        float sc[kNR][kG][4];
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt)
+        for (int nr = 0; nr < kNR; ++nr)
 #pragma unroll
-          for (int j = 0; j < kST; ++j)
+          for (int g = 0; g < kG; ++g)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sc[mt][j][i] = 0.f;
-        float kf[kST][2], vf[kST][2];
+            for (int i = 0; i < 4; ++i) sc[nr][g][i] = 0.f;
+        float kf[kG][2], vf[kG][2];
+        const uint32_t lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
         if constexpr (kFp8) {
 #pragma unroll
           for (int c = 0; c < D / 16; c += 2)
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
               uint32_t kr[4];
-              ldsm4(ak + swz<D, true>(16 * g + (lane & 7) + ((lane >> 3) & 1) * 8, c + (lane >> 4)), kr);
+              ldsm4(ak + swz<D, true>(16 * g + lrow, c + lchunk), kr);
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t a0 = expand2<0, 1>(kr[j]), a1 = expand2<2, 3>(kr[j]);
-                const uint32_t b0 = expand2<0, 1>(kr[2 + j]), b1 = expand2<2, 3>(kr[2 + j]);
+              for (int i = 0; i < 2; ++i) {
+                const uint32_t af[4] = {expand2<0, 1>(kr[2 * i]), expand2<0, 1>(kr[2 * i + 1]), expand2<2, 3>(kr[2 * i]),
+                                        expand2<2, 3>(kr[2 * i + 1])};
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) {
-                  mma16816<true>(sc[mt][2 * g + j], qf[mt][c], a0, a1);
-                  mma16816<true>(sc[mt][2 * g + j], qf[mt][c + 1], b0, b1);
-                }
+                for (int nr = 0; nr < kNR; ++nr) mma16816<true>(sc[nr][g], af, qf[nr][c + i][0], qf[nr][c + i][1]);
               }
             }
           // the largest of V's scales (0 where no key is)
@@ -335,21 +344,21 @@ __global__ void __launch_bounds__(256, 1)
             if (eref != kNoScale) {                       // rare: a scale far above the ones before
               const float f = exp2f((float)(eref - e));
 #pragma unroll
-              for (int mt = 0; mt < kMT; ++mt)
+              for (int nr = 0; nr < kNR; ++nr)
 #pragma unroll
-                for (int n = 0; n < kNT; ++n)
+                for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-                  for (int i = 0; i < 4; ++i) o[mt][n][i] *= f;
+                  for (int i = 0; i < 4; ++i) o[nr][n][i] *= f;
             }
             eref = e;
           }
           const float fk = scale_value(ck), fv = scale_value(max(cv + 127 - eref, 0));
 #pragma unroll
-          for (int j = 0; j < kST; ++j)
+          for (int g = 0; g < kG; ++g)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              kf[j][i] = __shfl_sync(0xffffffffu, fk, 8 * j + 2 * tq + i);
-              vf[j][i] = __shfl_sync(0xffffffffu, fv, 8 * j + 2 * tq + i);
+              kf[g][i] = __shfl_sync(0xffffffffu, fk, 16 * g + 8 * i + r0);
+              vf[g][i] = __shfl_sync(0xffffffffu, fv, 16 * g + 8 * i + r0);
             }
         } else {
 #pragma unroll
@@ -357,96 +366,71 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
               uint32_t kr[4];
-              ldsm4(ak + swz<D, false>(16 * g + (lane & 7) + (lane >> 4) * 8, 2 * kk + ((lane >> 3) & 1)), kr);
+              ldsm4(ak + swz<D, false>(16 * g + lrow, 2 * kk + lchunk), kr);
 #pragma unroll
-              for (int mt = 0; mt < kMT; ++mt) {
-                mma16816<kFp16>(sc[mt][2 * g], qf[mt][kk], kr[0], kr[1]);
-                mma16816<kFp16>(sc[mt][2 * g + 1], qf[mt][kk], kr[2], kr[3]);
-              }
+              for (int nr = 0; nr < kNR; ++nr) mma16816<kFp16>(sc[nr][g], kr, qf[nr][kk][0], qf[nr][kk][1]);
             }
         }
         // ---- scale, mask, online softmax
-        uint32_t pf[kMT][kG][4];
-        unsigned see[kMT][2];                             // bit 8j + i: key 8j + 2 tq + i is visible
+        uint32_t pp[kNR][kG][2];                          // P of keys r0 (+ 8), rows 2 tq, 2 tq + 1
+        uint32_t see[kNR][2];                             // bit k: key p0 + k is visible to the row
 #pragma unroll
-        for (int mt = 0; mt < kMT; ++mt) {
+        for (int nr = 0; nr < kNR; ++nr) {
 #pragma unroll
-          for (int hf = 0; hf < 2; ++hf) {
-            float x[kST][2];
-            see[mt][hf] = 0xFFFFFFFFu;
+          for (int e = 0; e < 2; ++e) {
+            float x[kG][2];
+            see[nr][e] = 0xFFFFFFFFu;
 #pragma unroll
-            for (int j = 0; j < kST; ++j)
+            for (int g = 0; g < kG; ++g)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) x[j][i] = sc[mt][j][2 * hf + i] * (kFp8 ? sl2[mt][hf] * kf[j][i] : sl2[mt][hf]);
+              for (int i = 0; i < 2; ++i) x[g][i] = sc[nr][g][2 * i + e] * (kFp8 ? sl2[nr][e] * kf[g][i] : sl2[nr][e]);
             if (masked) {
-              see[mt][hf] = visible32(a, s, tok[mt][hf], p0 - s.len) >> (2 * tq);
+              see[nr][e] = visible32(a, s, tok[nr][e], p0 - s.len);
 #pragma unroll
-              for (int j = 0; j < kST; ++j)
+              for (int g = 0; g < kG; ++g)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
-                  if (!((see[mt][hf] >> (8 * j + i)) & 1u)) x[j][i] = -INFINITY;
+                  if (!((see[nr][e] >> (16 * g + 8 * i + r0)) & 1u)) x[g][i] = -INFINITY;
             }
             float mx = fmaxf(x[0][0], x[0][1]);
 #pragma unroll
-            for (int j = 1; j < kST; ++j) mx = max3f(mx, x[j][0], x[j][1]);
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-            float mn = fmaxf(m[mt][hf], mx);
-            if (kFp8 && mn <= m[mt][hf] + 4.f) mn = m[mt][hf];    // (-inf stays -inf only when both are)
+            for (int g = 1; g < kG; ++g) mx = max3f(mx, x[g][0], x[g][1]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            float mn = fmaxf(m[nr][e], mx);
+            if (kFp8 && mn <= m[nr][e] + 4.f) mn = m[nr][e];      // (-inf stays -inf only when both are)
             const float neg = mn == -INFINITY ? 0.f : -mn;
-            const float al = ex2(m[mt][hf] + neg);        // 0 while m = -inf
-            m[mt][hf] = mn;
+            const float al = ex2(m[nr][e] + neg);         // 0 while m = -inf
+            m[nr][e] = mn;
             float sum = 0.f;
-            float p[kST][2];
 #pragma unroll
-            for (int j = 0; j < kST; ++j)
+            for (int g = 0; g < kG; ++g)
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                p[j][i] = ex2(x[j][i] + neg);
-                sum += p[j][i];
+                const float p = ex2(x[g][i] + neg);
+                sum += p;
+                sc[nr][g][2 * i + e] = kFp8 ? p * vf[g][i] : p;
               }
-            l[mt][hf] = l[mt][hf] * al + sum;
+            l[nr][e] = l[nr][e] * al + sum;
             if (__any_sync(0xffffffffu, al != 1.f)) {
 #pragma unroll
-              for (int n = 0; n < kNT; ++n) {
-                o[mt][n][2 * hf] *= al;
-                o[mt][n][2 * hf + 1] *= al;
+              for (int n = 0; n < D / 16; ++n) {
+                o[nr][n][e] *= al;
+                o[nr][n][2 + e] *= al;
               }
-            }
-            // P to 16 bits, one rounding of at most half a step (the row sum keeps 32 bits)
-#pragma unroll
-            for (int j = 0; j < kST; ++j) {
-              if constexpr (kFp8) {
-                p[j][0] *= vf[j][0];
-                p[j][1] *= vf[j][1];
-              }
-              pf[mt][j >> 1][hf + 2 * (j & 1)] = pack2<kMma16>(p[j][0], p[j][1]);
             }
           }
+          // P to 16 bits, one rounding of at most half a step (the row sum keeps 32 bits)
+#pragma unroll
+          for (int g = 0; g < kG; ++g)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) pp[nr][g][i] = pack2<kMma16>(sc[nr][g][2 * i], sc[nr][g][2 * i + 1]);
         }
-        // ---- O += P V
-        // V of a 16-key group, columns 32 c .. 32 c + 31 (E4M3) or 16 c .. 16 c + 15: kVT tiles of 8
-        constexpr int kVT = kFp8 ? 4 : 2;
-        auto vfrag = [&](int g, int c, uint32_t (&b)[kVT][2]) {
-          uint32_t vr[4];
-          ldsm4t(av + swz<D, kFp8>(16 * g + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * c + (lane >> 4)), vr);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {                   // keys 8 (i % 2) .., 16-byte chunk i / 2
-            if constexpr (kFp8) {
-              b[2 * (i >> 1)][i & 1] = expand2<0, 2>(vr[i]);
-              b[2 * (i >> 1) + 1][i & 1] = expand2<1, 3>(vr[i]);
-            } else {
-              b[i >> 1][i & 1] = vr[i];
-            }
-          }
-        };
-        // Past the sequence's last key the page holds anything: those rows of V count as zero.
-        auto keep = [&](int g, int i) -> uint32_t {       // of the keys in half i of group g's fragments
-          const int k = end - 16 * g - 2 * tq - 8 * i;
-          return (k > 0 ? 0xFFFFu : 0u) | (k > 1 ? 0xFFFF0000u : 0u);
-        };
-        // A masked product is 0 * v, which is not 0 where v is not finite: a step of new tokens
-        // whose values are not all finite makes its products one by one, visible keys only.
+        // ---- O^T += V^T P^T
+        // Past the sequence's last key the page holds anything: those rows of V count as zero.  A masked
+        // product is 0 * v, which is not 0 where v is not finite: a step of new tokens whose values
+        // are not all finite makes its products one by one, visible keys only.
         bool apart = false;
         if (masked) {
           // V's rows that exist, 16 bytes at a time over the warp
@@ -463,56 +447,73 @@ __global__ void __launch_bounds__(256, 1)
         if (apart) {
 #pragma unroll 1
           for (int key = 0; key < min(C::kKeys, end); ++key) {
-            const int src = (lane & ~3) | ((key & 7) >> 1), j = key >> 3, i = key & 1;
-            float w[kMT][2];
-            bool v[kMT][2];
+            const int src = ((key & 7) << 2) | tq, g = key >> 4, i = (key >> 3) & 1;
+            float2 w[kNR];
 #pragma unroll
-            for (int mt = 0; mt < kMT; ++mt)
+            for (int nr = 0; nr < kNR; ++nr) {
+              uint32_t pw = i ? pp[nr][0][1] : pp[nr][0][0];
+              if (kG > 1 && g == 1) pw = i ? pp[nr][kG - 1][1] : pp[nr][kG - 1][0];
+              w[nr] = unpack2<kMma16>(__shfl_sync(0xffffffffu, pw, src));
+            }
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                uint32_t pw = pf[mt][0][hf];              // tile j's pair of this lane's row
+            for (int n = 0; n < D / 16; ++n)
 #pragma unroll
-                for (int k = 1; k < kST; ++k)
-                  if (j == k) pw = pf[mt][k >> 1][hf + 2 * (k & 1)];
-                const float2 f = unpack2<kMma16>(__shfl_sync(0xffffffffu, pw, src));
-                w[mt][hf] = i ? f.y : f.x;
-                v[mt][hf] = (__shfl_sync(0xffffffffu, see[mt][hf], src) >> (8 * j + i)) & 1;
-              }
-#pragma unroll
-            for (int n = 0; n < kNT; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float x;                                  // V[key][column of accumulator (n, e)]
+              for (int k = 0; k < 2; ++k) {
+                float x;                                  // V[key][column of accumulators (n, 2 k ..)]
                 if constexpr (kFp8) {
-                  const int col = 16 * (n >> 1) + 4 * tq + 2 * e + (n & 1);
-                  x = unpack2<true>(e4m3_to_f16x2(sk[C::kHalf + swz<D, true>(key, col >> 4) + (col & 15)])).x;
+                  const int col = 2 * r0 + k;
+                  x = unpack2<true>(e4m3_to_f16x2(sk[C::kHalf + swz<D, true>(key, n) + col])).x;
                 } else {
-                  const int col = 8 * n + 2 * tq + e;
-                  x = unpack2<kFp16>(*reinterpret_cast<const uint16_t*>(sk + C::kHalf + swz<D, false>(key, col >> 3) +
-                                                                        2 * (col & 7))).x;
+                  x = unpack2<kFp16>(*reinterpret_cast<const uint16_t*>(sk + C::kHalf + swz<D, false>(key, 2 * n + k) + 2 * r0)).x;
                 }
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-                  for (int hf = 0; hf < 2; ++hf)
-                    if (v[mt][hf]) o[mt][n][2 * hf + e] += w[mt][hf] * x;
+                for (int nr = 0; nr < kNR; ++nr) {
+                  if ((see[nr][0] >> key) & 1u) o[nr][n][2 * k] += w[nr].x * x;
+                  if ((see[nr][1] >> key) & 1u) o[nr][n][2 * k + 1] += w[nr].y * x;
+                }
               }
           }
         } else {
 #pragma unroll
-          for (int c = 0; c < kNT / kVT; ++c)
+          for (int nr = 0; nr < kNR; ++nr)
+#pragma unroll
+            for (int g = 0; g < kG; ++g)
+#pragma unroll
+              for (int i = 0; i < 2; ++i) pp[nr][g][i] = transpose8(pp[nr][g][i]);
+          auto keep = [&](int g, int i) -> uint32_t {     // keys 16 g + 8 i + 2 tq, + 1
+            const int k = end - 16 * g - 2 * tq - 8 * i;
+            return (k > 0 ? 0xFFFFu : 0u) | (k > 1 ? 0xFFFF0000u : 0u);
+          };
+          constexpr int kStep = kFp8 ? 2 : 1;             // 16-column tiles of one load
+#pragma unroll
+          for (int n = 0; n < D / 16; n += kStep)
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
-              uint32_t b[kVT][2];
-              vfrag(g, c, b);
+              uint32_t vr[4], af[kStep][4];
+              if constexpr (kFp8) {
+                ldsm4t(av + swz<D, true>(16 * g + lrow, n + lchunk), vr);
+#pragma unroll
+                for (int i = 0; i < kStep; ++i) {
+                  af[i][0] = expand2<0, 2>(vr[2 * i]);
+                  af[i][1] = expand2<1, 3>(vr[2 * i]);
+                  af[i][2] = expand2<0, 2>(vr[2 * i + 1]);
+                  af[i][3] = expand2<1, 3>(vr[2 * i + 1]);
+                }
+              } else {
+                ldsm4t(av + swz<D, false>(16 * g + (lane & 7) + lchunk * 8, 2 * n + ((lane >> 3) & 1)), vr);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) af[0][i] = vr[i];
+              }
               if (masked) {
 #pragma unroll
-                for (int i = 0; i < 2 * kVT; ++i) b[i >> 1][i & 1] &= keep(g, i & 1);
+                for (int i = 0; i < kStep; ++i)
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) af[i][k] &= keep(g, k >> 1);
               }
 #pragma unroll
-              for (int i = 0; i < kVT; ++i)
+              for (int i = 0; i < kStep; ++i)
 #pragma unroll
-                for (int mt = 0; mt < kMT; ++mt) mma16816<kMma16>(o[mt][kVT * c + i], pf[mt][g], b[i][0], b[i][1]);
+                for (int nr = 0; nr < kNR; ++nr) mma16816<kMma16>(o[nr][n + i], af[i], pp[nr][g][0], pp[nr][g][1]);
             }
         }
       }
@@ -543,29 +544,32 @@ __global__ void __launch_bounds__(256, 1)
     float* stats = reinterpret_cast<float*>(smem_raw + C::kStats);       // [warp][m of 8 rows, l of 8 rows]
     int* es = reinterpret_cast<int*>(stats + 8 * 16);
 #pragma unroll
-    for (int mt = 0; mt < kMT; ++mt)
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int rb = mt * 16 + hf * 8;
+    for (int nr = 0; nr < kNR; ++nr) {
+        const int rb = nr * 8;
         if (rb >= nrows) continue;
-        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 1);
-        l[mt][hf] += __shfl_xor_sync(0xffffffffu, l[mt][hf], 2);
-        if (rb > 0) __syncthreads();                      // the rows before are summed
-        if constexpr (kFp8) {
 #pragma unroll
-          for (int c = 0; c < D / 16; ++c)
-            *reinterpret_cast<float4*>(so + r0 * C::kRowF + 16 * c + 4 * tq) =
-                make_float4(o[mt][2 * c][2 * hf], o[mt][2 * c + 1][2 * hf], o[mt][2 * c][2 * hf + 1],
-                            o[mt][2 * c + 1][2 * hf + 1]);
-        } else {
-#pragma unroll
-          for (int n = 0; n < kNT; ++n)
-            *reinterpret_cast<float2*>(so + r0 * C::kRowF + 8 * n + 2 * tq) =
-                make_float2(o[mt][n][2 * hf], o[mt][n][2 * hf + 1]);
+        for (int e = 0; e < 2; ++e) {
+          l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 4);
+          l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 8);
+          l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 16);
         }
-        if (tq == 0) {
-          stats[warp * 16 + r0] = m[mt][hf];
-          stats[warp * 16 + 8 + r0] = l[mt][hf];
+        if (rb > 0) __syncthreads();                      // the rows before are summed
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float* row = so + (2 * tq + e) * C::kRowF;
+#pragma unroll
+          for (int n = 0; n < D / 16; ++n) {
+            if constexpr (kFp8) {
+              *reinterpret_cast<float2*>(row + 16 * n + 2 * r0) = make_float2(o[nr][n][e], o[nr][n][2 + e]);
+            } else {
+              row[16 * n + r0] = o[nr][n][e];
+              row[16 * n + 8 + r0] = o[nr][n][2 + e];
+            }
+          }
+          if (r0 == 0) {
+            stats[warp * 16 + 2 * tq + e] = m[nr][e];
+            stats[warp * 16 + 8 + 2 * tq + e] = l[nr][e];
+          }
         }
         if (kFp8 && lane == 0) es[warp] = eref;
         __syncthreads();
@@ -687,9 +691,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   for (int j = 0; j < kV; j += 2) op[j / 2] = pack2<kFp16>(acc[j] * inv, acc[j + 1] * inv);
 }
 
-template <int D, bool kFp8, bool kFp16, int kMT>
+template <int D, bool kFp8, bool kFp16, int kNR>
 cudaError_t launch_small(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, cudaStream_t s) {
-  auto kern = tree_small_kernel<D, kFp8, kFp16, kMT>;
+  auto kern = tree_small_kernel<D, kFp8, kFp16, kNR>;
   constexpr int smem = SmallCfg<D, kFp8>::kSmem;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
@@ -698,16 +702,17 @@ cudaError_t launch_small(const CUtensorMap& tk, const CUtensorMap& tv, const Tre
 }
 
 template <int D, bool kFp8, bool kFp16>
-cudaError_t launch_small_mt(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, cudaStream_t s) {
-  return a.tile_rows == 16 ? launch_small<D, kFp8, kFp16, 1>(tk, tv, a, ctas, s)
-                           : launch_small<D, kFp8, kFp16, 2>(tk, tv, a, ctas, s);
+cudaError_t launch_small_nr(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, cudaStream_t s) {
+  return a.tile_rows == 8    ? launch_small<D, kFp8, kFp16, 1>(tk, tv, a, ctas, s)
+         : a.tile_rows == 16 ? launch_small<D, kFp8, kFp16, 2>(tk, tv, a, ctas, s)
+                             : launch_small<D, kFp8, kFp16, 4>(tk, tv, a, ctas, s);
 }
 
 template <int D>
 cudaError_t launch_small_d(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp8, bool fp16,
                            int ctas, cudaStream_t s) {
-  if (fp8) return fp16 ? launch_small_mt<D, true, true>(tk, tv, a, ctas, s) : launch_small_mt<D, true, false>(tk, tv, a, ctas, s);
-  return fp16 ? launch_small_mt<D, false, true>(tk, tv, a, ctas, s) : launch_small_mt<D, false, false>(tk, tv, a, ctas, s);
+  if (fp8) return fp16 ? launch_small_nr<D, true, true>(tk, tv, a, ctas, s) : launch_small_nr<D, true, false>(tk, tv, a, ctas, s);
+  return fp16 ? launch_small_nr<D, false, true>(tk, tv, a, ctas, s) : launch_small_nr<D, false, false>(tk, tv, a, ctas, s);
 }
 
 // Launched so that its blocks may start while the attention kernel still runs (they wait for its
@@ -744,7 +749,7 @@ TreeLayout tree_layout(int rows, int d) {
 
 // Most rows a row tile can have in a call with this many new tokens.
 int most_rows(int total, int G) {
-  const long long r = ((long long)total * G + 15) / 16 * 16;
+  const long long r = ((long long)total * G + 7) / 8 * 8;
   return (int)(r < kBigRows ? r : kBigRows);
 }
 
@@ -809,7 +814,7 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   a.scale_log2 = (float)((double)x.scale * 1.4426950408889634);
   const long long unit = (long long)min(x.max_new, x.total) * G;   // most rows of a key head
   const bool big = unit > 32;
-  a.tile_rows = big ? kBigRows : unit <= 16 ? 16 : 32;
+  a.tile_rows = big ? kBigRows : unit <= 8 ? 8 : unit <= 16 ? 16 : 32;
   a.slot_rows = min(a.tile_rows, most_rows(x.total, G));
   a.chunk_shift = !big && x.cache.d * (fp8 ? 1 : 2) <= 128 ? 8 : 7;   // 32-key steps: SmallCfg
 
