@@ -285,6 +285,11 @@ __device__ __forceinline__ uint32_t visible32(const TreeArgs& a, const SeqView& 
   return k < 32 ? v & ((1u << k) - 1u) : v;
 }
 
+template <int N>
+__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // Host side (fa_cache.cu): checks of the cache argument, and its view.
 int check_cache(const fa_cache& c);
 CacheView view_of(const fa_cache& c);

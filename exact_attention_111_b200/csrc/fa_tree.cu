@@ -7,11 +7,12 @@
 // in one pass over the keys with a running max m and sum l (online softmax).
 //
 // This file's kernel is the one for few rows per key head (decoding, small trees), where the cache is
-// read once and its bytes are the bound.  One CTA per SM, eight warps.  A chunk of 128 keys is
-// eight steps of 16 keys; warp w always takes step w, with a ring of its own that its lane 0 fills by
-// TMA several steps ahead, so warps never wait for one another inside a segment and loads cross
-// from one unit to the next without a pause.  Each warp keeps its own m, l and O; at the end of a
-// segment (the CTA's run of chunks of one unit) the eight are merged through shared memory.
+// read once and its bytes are the bound.  One CTA per SM, eight warps that compute and two that load.  A
+// chunk is eight steps of 16 or 32 keys, 32 or 64 KB in all, copied by TMA in boxes of whole pages into a ring
+// that runs several chunks ahead and on into the next unit; warp w always takes step w.  Each warp
+// keeps its own m, l and O; at the end of a segment (the CTA's run of chunks of one unit) the
+// eight are merged through shared memory.  (With a ring of its own for each warp, filled by the warp, the
+// copies' issue took 700 of a step's 2000 cycles; a ninth warp filling the eight rings was the bottleneck.)
 //
 // The products are made transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): keys and columns
 // fill the 16-wide side and rows come in eights, so four or eight query heads of a group cost
@@ -69,9 +70,9 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
   }
 }
 
-// Asynchronous copy of n <= 4 bytes (the rest of the four zeros), and its arrival on a barrier.
-__device__ __forceinline__ void copy4(void* dst, const void* src, uint32_t n) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
+// Asynchronous copy of n <= 16 bytes (the rest of the sixteen zeros), and its arrival on a barrier.
+__device__ __forceinline__ void copy16(void* dst, const void* src, uint32_t n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -88,33 +89,38 @@ __device__ __forceinline__ uint32_t expand2(uint32_t w) {
 template <int D, bool kFp8>
 struct SmallCfg {
   static constexpr int kEsz = kFp8 ? 1 : 2;
-  // Keys of a step.  32 where a row is at most 128 bytes: the fixed work of a step (its copies, row
-  // max and rescale) is then spent on 8 KB as with 16 rows of 256 bytes.
+  // Keys of a step.  32 where a row is at most 128 bytes: the fixed work of a step (row max, rescale) is
+  // then spent on as many bytes as with 16 rows of 256.
   static constexpr int kKeys = D * kEsz <= 128 ? 32 : 16;
   static constexpr int kChunkKeys = 8 * kKeys;           // a chunk: one step of each warp
-  static constexpr int kHalf = kKeys * D * kEsz;         // K (or V) of a step
+  static constexpr int kHalf = kChunkKeys * D * kEsz;    // K (or V) of a chunk
   static constexpr int kStage = 2 * kHalf;
-  static constexpr int kStages = kFp8 && D == 128 ? 2 : 24576 / kStage;
-  static constexpr int kRing = 8 * kStages * kStage;     // all warps
-  // Merge of the eight warps, eight rows at a time: each warp's O rows (4 floats apart beyond D: the
-  // fragments' stores then hit all banks), m and l of its rows, and E.
-  static constexpr int kRowF = D + 4;
+  static constexpr int kStages = 3 * 65536 / kStage;
+  static constexpr int kRing = kStages * kStage;
+  // Merge of the eight warps, eight rows at a time: each warp's O rows (a few floats apart beyond D, so
+  // that the fragments' stores spread over the banks), m and l of its rows, and E.
+  static constexpr int kRowF = D + (kFp8 ? 2 : 4);
   static constexpr int kSlotF = 8 * kRowF;
   static constexpr int kMerge = kRing, kStats = kMerge + 8 * kSlotF * 4, kBars = kStats + 8 * 16 * 4 + 8 * 4;
-  // E4M3: the steps' scale codes, K's then V's
-  static constexpr int kCodes = kBars + 8 * kStages * 8 + 16;
-  static constexpr int kSmem = kCodes + (kFp8 ? 8 * kStages * 2 * kKeys : 0);
+  // E4M3: the chunks' scale codes, K's then V's
+  static constexpr int kCodes = kBars + 2 * kStages * 8 + 16;
+  static constexpr int kSmem = kCodes + (kFp8 ? kStages * 2 * kChunkKeys : 0);
   static_assert(kSmem <= 227 * 1024, "shared memory");
-  // bytes between 16-byte chunks' rows: 128-byte panels (64-byte rows for E4M3 at d = 64)
-  static constexpr int kRowB = D * kEsz < 128 ? 64 : 128;
+  static_assert(kCodes % 16 == 0, "16-byte copies");
+  // 384 threads (the loading warps' warpgroup is completed by two idle ones) x 168 registers at launch,
+  // shared out again by setmaxnreg.
+  static constexpr int kLaunchRegs = 168, kRegCompute = 216, kRegLoad = 72;
+  static_assert(2 * kRegCompute + kRegLoad <= 3 * kLaunchRegs, "register shares");
+  static constexpr int kRowB = D * kEsz < 128 ? 64 : 128; // bytes between rows of a 128-byte panel (64-byte rows)
 };
 
-// Shared-memory offset of 16-byte chunk c of row r of K or V of a step as TMA wrote it.
+// Shared-memory offset of 16-byte chunk c of row r of a step as TMA wrote it; panel: bytes between the
+// two 128-byte panels of 256-byte rows.
 template <int D, bool kFp8>
-__device__ __forceinline__ uint32_t swz(int r, int c) {
-  // (two panels only with 16 keys, one copy)
+__device__ __forceinline__ uint32_t swz(int r, int c, int panel) {
   if constexpr (SmallCfg<D, kFp8>::kRowB == 64) return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-  else return (c >> 3) * 2048 + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  else if constexpr (D * SmallCfg<D, kFp8>::kEsz == 128) return r * 128 + ((c ^ (r & 7)) << 4);
+  else return (c >> 3) * panel + r * 128 + (((c & 7) ^ (r & 7)) << 4);
 }
 
 // kFp16: type of q and o.  A 16-bit cache's products are in that type.  An E4M3 cache's are in fp16, which
@@ -126,7 +132,7 @@ __device__ __forceinline__ uint32_t swz(int r, int c) {
 // row's max grows in almost every one.  bf16 queries enter as fp16 with a power of two for each row
 // (row_factor).
 template <int D, bool kFp8, bool kFp16, int kNR>
-__global__ void __launch_bounds__(256, 1)
+__global__ void __launch_bounds__(384, 1)
     tree_small_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                       const TreeArgs a) {
   using C = SmallCfg<D, kFp8>;
@@ -138,92 +144,102 @@ __global__ void __launch_bounds__(256, 1)
     return;
   }
   const int warp = warp_id(), lane = lane_id();
-  uint8_t* ring = smem_raw + warp * C::kStages * C::kStage;
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + C::kBars) + warp * C::kStages;
-  volatile int* abort_flag = reinterpret_cast<int*>(smem_raw + C::kBars + 8 * C::kStages * 8);
-  uint8_t* codes = smem_raw + C::kCodes + warp * C::kStages * 2 * C::kKeys;
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem_raw + C::kBars);
+  uint64_t* empty = full + C::kStages;
+  volatile int* abort_flag = reinterpret_cast<int*>(empty + C::kStages);
   const DevStatus st{a.c.status, a.timeout_ns};
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  if (lane == 0)
-    for (int i = 0; i < C::kStages; ++i) mbar_init(&full[i], kFp8 ? 33 : 1);
+  if (threadIdx.x < C::kStages) {
+    mbar_init(&full[threadIdx.x], kFp8 ? 2 + 2 * C::kChunkKeys / 16 : 2);         // both loaders, and their lanes that copy codes
+    mbar_init(&empty[threadIdx.x], 8);
+  }
   if (threadIdx.x == 0) {
     *abort_flag = 0;
-    prefetch_tmap(&tm_k);
-    prefetch_tmap(&tm_v);
     a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   }
   fence_barrier_init();
   const Part part = find_part(a, blockIdx.x == 0 && warp == 0);
   if (part.n == 0) return;
-  Cursor rd = part.at, ld = rd;
-  int rd_left = part.n, ld_left = part.n;
   __syncthreads();
 
-  // ---------------------------------------------------------------- loads
-  // A step is loaded when its first key exists and some row of the tile may see it.  `ld` stands at
-  // the next step to load; lane i's page id for its key p0 + i is on its way since the last.
-  auto wanted = [&](const Cursor& c) { return c.kt * C::kChunkKeys + warp * C::kKeys <= c.last; };
-  int page = 0;
-  auto advance = [&](Cursor& c, int& left) {
-    --left;
-    if (++c.kt < c.s.KT) return;
-    if (left > 0) next_unit(a, c);
-  };
-  auto look_up = [&]() {
-    while (ld_left > 0 && !wanted(ld)) advance(ld, ld_left);
-    if (ld_left > 0) {
-      const int pos = ld.kt * C::kChunkKeys + warp * C::kKeys + (lane & (C::kKeys - 1));
-      if (pos < ld.s.len + ld.s.T) page = a.c.table[(long long)ld.b * a.c.table_stride + (pos >> a.c.page_shift)];
-    }
-  };
-  int fs = 0;                                             // stage to fill
-  auto fill = [&]() {                                     // start the copies of the step `ld` stands at
-    const int pos = ld.kt * C::kChunkKeys + warp * C::kKeys + (lane & (C::kKeys - 1));
-    const bool key = pos < ld.s.len + ld.s.T;
-    int row = (a.c.pages * a.c.Hk) << a.c.page_shift;     // past the end: a row behind the tensor reads as zeros
-    if (key) {
-      if ((unsigned)page >= (unsigned)a.c.pages) {
-        flag_range(a.c);
-        page = 0;                                         // stay inside the cache
-      }
-      row = ((page * a.c.Hk + ld.h) << a.c.page_shift) + (pos & ((1 << a.c.page_shift) - 1));
-    }
-    const int row2 = C::kKeys == 32 ? __shfl_sync(0xffffffffu, row, 16) : 0;
-    uint64_t* bar = &full[fs];
-    if (lane == 0) {
-      uint8_t* dst = ring + fs * C::kStage;
-      mbar_arrive_expect_tx(bar, C::kStage);
-      tma_load_3d(dst, &tm_k, bar, 0, row, 0);
-      tma_load_3d(dst + C::kHalf, &tm_v, bar, 0, row, 0);
-      if (C::kKeys == 32 && a.c.page_shift == 4) {        // boxes of 16 rows: two
-        tma_load_3d(dst + C::kHalf / 2, &tm_k, bar, 0, row2, 0);
-        tma_load_3d(dst + C::kHalf + C::kHalf / 2, &tm_v, bar, 0, row2, 0);
-      }
-    }
-    if constexpr (kFp8) {
-      // scale codes, four keys a lane and set (zeros past the end); the barrier counts the lanes too
-      if ((lane & 3) == 0) {
-        const int left = ld.s.len + ld.s.T - pos;         // keys from this one on
-        const uint32_t n = left >= 4 ? 4 : left <= 0 ? 0 : left;
-        const int src = n > 0 ? row : 0;
-        copy4(codes + fs * 2 * C::kKeys + lane, a.c.ks + src, n);
-        copy4(codes + (fs * 2 + 1) * C::kKeys + lane, a.c.vs + src, n);
-      }
-      copy_arrive(bar);
-    }
-    __syncwarp();
-    fs = fs + 1 == C::kStages ? 0 : fs + 1;
-    advance(ld, ld_left);
+  if (warp >= 8) {
+    reg_dec<C::kRegLoad>();
+    if (warp > 9) return;
+    // ---------------------------------------------------------------- loads: warp 8 K, warp 9 V
+    // One chunk at a time: lane i looks up the page of the chunk's 16-key group i (one chunk ahead).  A
+    // chunk is loaded when some row of the tile may see its first key.
+    const CUtensorMap* map = warp == 8 ? &tm_k : &tm_v;
+    const uint8_t* scales = warp == 8 ? a.c.ks : a.c.vs;
+    if (lane == 0) prefetch_tmap(map);
+    constexpr int kGroups = C::kChunkKeys / 16;
+    const int per_box = 1 << (a.c.page_shift - 4);        // groups of a page, and of a copy
+    Cursor c = part.at;
+    int page = 0;
+    auto look_up = [&]() {
+      const int pos = c.kt * C::kChunkKeys + 16 * lane;
+      if (lane < kGroups && pos < c.s.len + c.s.T)
+        page = a.c.table[(long long)c.b * a.c.table_stride + (pos >> a.c.page_shift)];
+    };
     look_up();
-  };
-  look_up();
-  int issued = 0;
-  for (; issued < C::kStages && ld_left > 0; ++issued) fill();
+    int stg = 0, phase = 1, count = 0;                    // chunks loaded
+    bool ok = true;
+    for (int n = part.n; n > 0 && ok; --n) {
+      const int end = c.s.len + c.s.T - c.kt * C::kChunkKeys;     // keys of the chunk from here on do not exist
+      int row = (a.c.pages * a.c.Hk) << a.c.page_shift;   // lane's group; past the end: a row behind the
+      if (lane < kGroups && 16 * lane < end) {            // tensor reads as zeros
+        if ((unsigned)page >= (unsigned)a.c.pages) {
+          flag_range(a.c);
+          page = 0;                                       // stay inside the cache
+        }
+        const int pos = c.kt * C::kChunkKeys + 16 * lane;
+        row = ((page * a.c.Hk + c.h) << a.c.page_shift) + (pos & ((1 << a.c.page_shift) - 1));
+      }
+      const bool wanted = c.kt * C::kChunkKeys <= c.last;
+      c.kt++;
+      if (n > 1) {
+        if (c.kt == c.s.KT) next_unit(a, c);
+        look_up();
+      }
+      if (!wanted) continue;
+      if (count >= C::kStages) ok = mbar_wait(&empty[stg], phase, abort_flag, st);
+      if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+      if (lane == 0) mbar_arrive_expect_tx(&full[stg], C::kHalf);
+      __syncwarp();
+      uint8_t* dst = smem_raw + stg * C::kStage + (warp == 9 ? C::kHalf : 0);
+      if (lane < kGroups && lane % per_box == 0) tma_load_3d(dst + lane * 16 * D * C::kEsz, map, &full[stg], 0, row, 0);
+      if constexpr (kFp8) {
+        if (lane < kGroups) {                             // scale codes, zeros past the end
+          const int bytes = min(16, max(0, end - 16 * lane));
+          copy16(smem_raw + C::kCodes + (stg * 2 + warp - 8) * C::kChunkKeys + 16 * lane, scales + (bytes > 0 ? row : 0), bytes);
+          copy_arrive(&full[stg]);
+        }
+      }
+      ++count;
+      if (++stg == C::kStages) {
+        stg = 0;
+        phase ^= 1;
+      }
+    }
+    // A wait that ran out left copies in flight: let them land before the shared memory goes away.
+    if (*abort_flag && lane == 0)
+      for (int i = max(0, count - C::kStages); i < count; ++i)
+        mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1, st);
+    return;
+  }
+
+  reg_inc<C::kRegCompute>();
+  // this warp's keys in a stage: in a page's copy the panels of 256-byte rows stand one after the other
+  const int page_rows = 1 << a.c.page_shift, key0 = warp * C::kKeys;
+  const int panel = page_rows * 128;
+  const int mine = D * C::kEsz > 128 ? (key0 >> a.c.page_shift) * page_rows * (D * C::kEsz) + (key0 & (page_rows - 1)) * 128
+                                     : key0 * D * C::kEsz;
+  Cursor rd = part.at;
+  int rd_left = part.n;
 
   // ---------------------------------------------------------------- segments
   const int r0 = lane >> 2, tq = lane & 3;                // fragment row and column quad
-  int us = 0, uphase = 0, used = 0;                       // stage to use, its parity
+  int us = 0, uphase = 0;                                 // stage to use, its parity
   bool ok = true;
   while (rd_left > 0) {
     const SeqView s = rd.s;
@@ -302,12 +318,12 @@ __global__ void __launch_bounds__(256, 1)
     // Unit, sequence and head stay; only kt moves until the unit or the part ends.
     const int kt_end = min(s.KT, rd.kt + min(rd_left, s.KT));
     for (int kt = rd.kt; kt < kt_end; ++kt) {
-      const int p0 = kt * C::kChunkKeys + warp * C::kKeys;
-      if (p0 > rd.last) continue;
+      const int p0 = kt * C::kChunkKeys + key0;
+      if (kt * C::kChunkKeys > rd.last) break;            // nor is any chunk after it
       if (ok) ok = mbar_wait(&full[us], uphase, abort_flag, st);
       ok = __all_sync(0xffffffffu, ok);
-      if (ok) {
-        const uint8_t* sk = ring + us * C::kStage;
+      if (ok && p0 <= rd.last) {
+        const uint8_t* sk = smem_raw + us * C::kStage + mine;
         const uint32_t ak = smem_addr(sk), av = ak + C::kHalf;
         const int end = s.len + s.T - p0;                 // keys of the step from here on do not exist
         const bool masked = p0 + C::kKeys > s.len;
@@ -320,14 +336,14 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[nr][g][i] = 0.f;
         float kf[kG][2], vf[kG][2];
-        const uint32_t lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
+        const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
         if constexpr (kFp8) {
 #pragma unroll
           for (int c = 0; c < D / 16; c += 2)
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
               uint32_t kr[4];
-              ldsm4(ak + swz<D, true>(16 * g + lrow, c + lchunk), kr);
+              ldsm4(ak + swz<D, true>(16 * g + lrow, c + lchunk, panel), kr);
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 const uint32_t af[4] = {expand2<0, 1>(kr[2 * i]), expand2<0, 1>(kr[2 * i + 1]), expand2<2, 3>(kr[2 * i]),
@@ -337,7 +353,8 @@ __global__ void __launch_bounds__(256, 1)
               }
             }
           // the largest of V's scales (0 where no key is)
-          const int ck = codes[us * 2 * C::kKeys + lane], cv = codes[(us * 2 + 1) * C::kKeys + lane];
+          const int ck = smem_raw[C::kCodes + us * 2 * C::kChunkKeys + key0 + lane];
+          const int cv = smem_raw[C::kCodes + (us * 2 + 1) * C::kChunkKeys + key0 + lane];
           const int top = (int)__reduce_max_sync(0xffffffffu, (unsigned)cv);
           if (top > eref + 11) {
             const int e = top - 8;
@@ -366,7 +383,7 @@ __global__ void __launch_bounds__(256, 1)
 #pragma unroll
             for (int g = 0; g < kG; ++g) {
               uint32_t kr[4];
-              ldsm4(ak + swz<D, false>(16 * g + lrow, 2 * kk + lchunk), kr);
+              ldsm4(ak + swz<D, false>(16 * g + lrow, 2 * kk + lchunk, panel), kr);
 #pragma unroll
               for (int nr = 0; nr < kNR; ++nr) mma16816<kFp16>(sc[nr][g], kr, qf[nr][kk][0], qf[nr][kk][1]);
             }
@@ -438,7 +455,7 @@ __global__ void __launch_bounds__(256, 1)
           bool bad = false;
 #pragma unroll 1
           for (int i = lane; i < min(C::kKeys, end) * kC; i += 32) {
-            const uint4 x = *reinterpret_cast<const uint4*>(sk + C::kHalf + swz<D, kFp8>(i / kC, i % kC));
+            const uint4 x = *reinterpret_cast<const uint4*>(sk + C::kHalf + swz<D, kFp8>(i / kC, i % kC, panel));
             bad |= not_finite<kFp8, kFp16>(x.x) || not_finite<kFp8, kFp16>(x.y) || not_finite<kFp8, kFp16>(x.z) ||
                    not_finite<kFp8, kFp16>(x.w);
           }
@@ -462,9 +479,9 @@ __global__ void __launch_bounds__(256, 1)
                 float x;                                  // V[key][column of accumulators (n, 2 k ..)]
                 if constexpr (kFp8) {
                   const int col = 2 * r0 + k;
-                  x = unpack2<true>(e4m3_to_f16x2(sk[C::kHalf + swz<D, true>(key, n) + col])).x;
+                  x = unpack2<true>(e4m3_to_f16x2(sk[C::kHalf + swz<D, true>(key, n, panel) + col])).x;
                 } else {
-                  x = unpack2<kFp16>(*reinterpret_cast<const uint16_t*>(sk + C::kHalf + swz<D, false>(key, 2 * n + k) + 2 * r0)).x;
+                  x = unpack2<kFp16>(*reinterpret_cast<const uint16_t*>(sk + C::kHalf + swz<D, false>(key, 2 * n + k, panel) + 2 * r0)).x;
                 }
 #pragma unroll
                 for (int nr = 0; nr < kNR; ++nr) {
@@ -491,7 +508,7 @@ __global__ void __launch_bounds__(256, 1)
             for (int g = 0; g < kG; ++g) {
               uint32_t vr[4], af[kStep][4];
               if constexpr (kFp8) {
-                ldsm4t(av + swz<D, true>(16 * g + lrow, n + lchunk), vr);
+                ldsm4t(av + swz<D, true>(16 * g + lrow, n + lchunk, panel), vr);
 #pragma unroll
                 for (int i = 0; i < kStep; ++i) {
                   af[i][0] = expand2<0, 2>(vr[2 * i]);
@@ -500,7 +517,7 @@ __global__ void __launch_bounds__(256, 1)
                   af[i][3] = expand2<1, 3>(vr[2 * i + 1]);
                 }
               } else {
-                ldsm4t(av + swz<D, false>(16 * g + (lane & 7) + lchunk * 8, 2 * n + ((lane >> 3) & 1)), vr);
+                ldsm4t(av + swz<D, false>(16 * g + (lane & 7) + lchunk * 8, 2 * n + ((lane >> 3) & 1), panel), vr);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) af[0][i] = vr[i];
               }
@@ -517,14 +534,10 @@ __global__ void __launch_bounds__(256, 1)
             }
         }
       }
+      __syncwarp();                                       // the stage has been read
+      if (lane == 0) mbar_arrive(&empty[us]);
       us = us + 1 == C::kStages ? 0 : us + 1;
       if (us == 0) uphase ^= 1;
-      ++used;
-      __syncwarp();                                       // the stage has been read: refill it
-      if (ok && ld_left > 0) {
-        fill();
-        ++issued;
-      }
     }
     const bool to_end = kt_end == s.KT;
     rd_left -= kt_end - rd.kt;
@@ -553,7 +566,7 @@ __global__ void __launch_bounds__(256, 1)
           l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 8);
           l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 16);
         }
-        if (rb > 0) __syncthreads();                      // the rows before are summed
+        if (rb > 0) named_bar_sync(1, 256);                      // the rows before are summed
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float* row = so + (2 * tq + e) * C::kRowF;
@@ -572,7 +585,7 @@ __global__ void __launch_bounds__(256, 1)
           }
         }
         if (kFp8 && lane == 0) es[warp] = eref;
-        __syncthreads();
+        named_bar_sync(1, 256);
         const int r = rb + warp;
         if (r < nrows) {
           constexpr int kV = D / 32;                      // columns of a lane
@@ -618,13 +631,9 @@ __global__ void __launch_bounds__(256, 1)
           }
         }
       }
-    if (rd_left > 0) __syncthreads();                     // the last rows are summed
+    if (rd_left > 0) named_bar_sync(1, 256);                     // the last rows are summed
     if (rd_left > 0) next_unit(a, rd);
   }
-  // A wait that ran out left copies in flight: let them land before the shared memory goes away.
-  if (!ok && lane == 0)
-    for (int i = max(used, issued - C::kStages); i < issued; ++i)
-      mbar_wait_drain(&full[i % C::kStages], (i / C::kStages) & 1, st);
 }
 
 // ------------------------------------------------------------------------------------
@@ -697,7 +706,17 @@ cudaError_t launch_small(const CUtensorMap& tk, const CUtensorMap& tv, const Tre
   constexpr int smem = SmallCfg<D, kFp8>::kSmem;
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, 256, smem, s>>>(tk, tv, a);
+  // setmaxnreg.inc waits until the block's launch registers cover every warpgroup's share: refuse a
+  // build whose register count differs from the one the shares assume.
+  static int regs = 0;
+  if (regs == 0) {
+    cudaFuncAttributes at;
+    const cudaError_t f = cudaFuncGetAttributes(&at, kern);
+    if (f != cudaSuccess) return f;
+    regs = at.numRegs;
+  }
+  if (regs != SmallCfg<D, kFp8>::kLaunchRegs) return cudaErrorInvalidConfiguration;
+  kern<<<ctas, 384, smem, s>>>(tk, tv, a);
   return cudaGetLastError();
 }
 
@@ -819,10 +838,9 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   a.chunk_shift = !big && x.cache.d * (fp8 ? 1 : 2) <= 128 ? 8 : 7;   // 32-key steps: SmallCfg
 
   CUtensorMap tk, tv;
-  const int box = big || a.chunk_shift == 7 ? (big ? x.cache.page_size : 16) : min(x.cache.page_size, 32);   // rows of a copy
   const long long rows = (long long)x.cache.pages * x.cache.Hk * x.cache.page_size;
-  if (!encode_cache(&tk, x.cache.k, rows, x.cache.d, fp8 ? 1 : 2, box, !big) ||
-      !encode_cache(&tv, x.cache.v, rows, x.cache.d, fp8 ? 1 : 2, box, !big))
+  if (!encode_cache(&tk, x.cache.k, rows, x.cache.d, fp8 ? 1 : 2, x.cache.page_size, !big) ||
+      !encode_cache(&tv, x.cache.v, rows, x.cache.d, fp8 ? 1 : 2, x.cache.page_size, !big))
     return FA_ERR_CUDA;
   // One CTA per SM, fewer where the longest possible sequences have fewer chunks.
   const long long kt = (((long long)x.cache.max_pages * x.cache.page_size - 1) >> a.chunk_shift) + 1;

@@ -105,11 +105,6 @@ struct BigShared {
   Walk walk[8];                  // one per softmax warp, whose registers are full
 };
 
-template <int N>
-__device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N>
-__device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
-
 // Whether tile kt holds new tokens or reaches past them.
 __device__ __forceinline__ bool tail_tile(const Seg& e, int kt) { return (kt + 1) * kChunk > e.s.len; }
 
