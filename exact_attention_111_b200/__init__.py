@@ -49,6 +49,7 @@ FA_MAX_PARTS = 64
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libfa.so")
 _lib = None
+_torch = None          # set by the first KVCache, which every serving call needs
 
 _vp = ctypes.c_void_p
 _i = ctypes.c_int
@@ -529,7 +530,9 @@ class KVCache:
     between calls.  The object keeps the tensors alive and allocates nothing."""
 
     def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
+        global _torch
         import torch
+        _torch = torch
         for t in (k, v):
             if not (t.is_cuda and t.is_contiguous() and t.dim() == 4 and t.shape == k.shape and t.dtype == k.dtype):
                 raise ValueError("expected k and v as contiguous CUDA tensors of one type, [pages, Hk, page_size, d]")
@@ -562,20 +565,20 @@ class KVCache:
         self.args = bytes(args)
         self._per_sequence, self._bounds = (self.B,), (self.B + 1,)
 
-    def _lengths(self, name, t, shape):
-        import torch
-        if not (t.get_device() == self.index and t.dtype is torch.int32 and t.shape == shape and t.is_contiguous()):
-            raise ValueError(f"expected {name} as a contiguous int32 tensor {list(shape)} on the cache's device")
+    def _ints(self, **named):
+        """Check int32 tensors given as name=(tensor, shape)."""
+        for name, (t, shape) in named.items():
+            if not (t.dtype is _torch.int32 and t.shape == shape and t.is_contiguous() and t.get_device() == self.index):
+                raise ValueError(f"expected {name} as a contiguous int32 tensor {list(shape)} on the cache's device")
 
     def _rows(self, name, t, heads):
-        """(token, head) strides of a [total, heads, d] tensor; heads None: any multiple of Hk."""
+        """(token, head) strides of a [total, heads, d] tensor."""
         shape = t.shape
-        if (t.get_device() == self.index and len(shape) == 3 and shape[2] == self.d
-                and (shape[1] == heads if heads is not None else shape[1] > 0 and shape[1] % self.Hk == 0)):
+        if len(shape) == 3 and shape[1] == heads and shape[2] == self.d and t.get_device() == self.index:
             st, sh, sd = t.stride()
             if sd == 1:
-                return st if shape[0] > 1 else 0, sh if shape[1] > 1 else 0
-        raise ValueError(f"expected {name} as [total, heads, {self.d}] on the cache's device, its last dimension contiguous")
+                return st if shape[0] > 1 else 0, sh if heads > 1 else 0
+        raise ValueError(f"expected {name} as [total, {heads}, {self.d}] on the cache's device, its last dimension contiguous")
 
     def _type(self, t):
         code = _dtype_code(t)
@@ -583,49 +586,56 @@ class KVCache:
             raise TypeError(f"{t.dtype} tensors with a cache of {self.k.dtype}")
         return code
 
+    def _raw_stream(self, stream):
+        """The stream's handle; the current stream of the cache's device by default."""
+        if stream is None:
+            return _torch._C._cuda_getCurrentRawStream(self.index)
+        return _stream(stream)
 
-def _on_device(cache, call, *args, stream=None):
-    """Run ``call`` on ``stream``, or the current stream of the cache's device, with that device
-    current (CUDA launches go to the current device)."""
-    import torch
-    if stream is None:
-        stream = torch._C._cuda_getCurrentRawStream(cache.index)
-    if cache.index == torch._C._cuda_getDevice():
-        return call(*args, stream)
-    with torch.cuda.device(cache.index):
-        return call(*args, stream)
+    def _call(self, name, payload):
+        """Call an entry point with the cache's device current (CUDA launches go to it)."""
+        f = getattr(_lib or lib(), name)
+        if self.index == _torch._C._cuda_getDevice():
+            rc = f(self.args + payload)
+        else:
+            with _torch.cuda.device(self.index):
+                rc = f(self.args + payload)
+        if rc:
+            raise FAError(rc, name)
 
 
 def cache_append(cache, k_new, v_new, cu_new, lens, stream=None):
     """Write the rows of new tokens, k_new and v_new [total, Hk, d] (bf16 or fp16; strided views
     will do), behind what each sequence holds (fa_cache_append): token cu_new[b] + i goes to position
     lens[b] + i of sequence b.  ``lens`` is not changed.  An E4M3 cache quantises them."""
-    ks, vs = cache._rows("k_new", k_new, cache.Hk), cache._rows("v_new", v_new, cache.Hk)
-    if v_new.shape[0] != k_new.shape[0] or v_new.dtype is not k_new.dtype:
+    kt, kh = cache._rows("k_new", k_new, cache.Hk)
+    vt, vh = cache._rows("v_new", v_new, cache.Hk)
+    total = len(k_new)
+    if len(v_new) != total or v_new.dtype is not k_new.dtype:
         raise ValueError("k_new and v_new differ in shape or type")
-    cache._lengths("cu_new", cu_new, cache._bounds)
-    cache._lengths("lens", lens, cache._per_sequence)
-    _on_device(cache, fa_cache_append, cache.args, k_new, v_new, ks, vs, cu_new, lens, k_new.shape[0],
-               cache._type(k_new), stream=stream)
+    cache._ints(cu_new=(cu_new, cache._bounds), lens=(lens, cache._per_sequence))
+    cache._call("fa_cache_append", _pack_append(
+        k_new.data_ptr(), v_new.data_ptr(), kt, kh, vt, vh, cu_new.data_ptr(), lens.data_ptr(), total,
+        cache._type(k_new), cache._raw_stream(stream)))
 
 
 def cache_read(cache, lens, N, dtype=None, k_out=None, v_out=None, stream=None):
     """The cache as dense (K, V), [B, Hk, N, d] 16-bit tensors with zeros past lens[b]
     (fa_cache_read).  ``dtype``: of an E4M3 cache's result, torch.bfloat16 (default) or float16;
     ``k_out``, ``v_out``: tensors to write to."""
-    import torch
-    cache._lengths("lens", lens, cache._per_sequence)
+    cache._ints(lens=(lens, cache._per_sequence))
     shape = (cache.B, cache.Hk, N, cache.d)
     if dtype is None:
-        dtype = k_out.dtype if k_out is not None else torch.bfloat16 if cache.dtype == FA_E4M3 else cache.k.dtype
+        dtype = k_out.dtype if k_out is not None else _torch.bfloat16 if cache.dtype == FA_E4M3 else cache.k.dtype
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        k_out = _torch.empty(shape, dtype=dtype, device=cache.device)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=cache.device)
+        v_out = _torch.empty(shape, dtype=dtype, device=cache.device)
     for t in (k_out, v_out):
         if not (t.get_device() == cache.index and t.shape == shape and t.is_contiguous() and t.dtype is dtype):
             raise ValueError(f"expected k_out and v_out as contiguous {dtype} tensors {list(shape)}")
-    _on_device(cache, fa_cache_read, cache.args, lens, k_out, v_out, N, cache._type(k_out), stream=stream)
+    cache._call("fa_cache_read", _pack_read(lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), N,
+                                            cache._type(k_out), cache._raw_stream(stream)))
     return k_out, v_out
 
 
@@ -636,10 +646,9 @@ def cache_keep(cache, lens, kept, counts, stream=None):
     if kept.dim() != 2:
         raise ValueError("expected kept as [B, width]")
     width = kept.shape[1]
-    cache._lengths("lens", lens, cache._per_sequence)
-    cache._lengths("kept", kept, (cache.B, width))
-    cache._lengths("counts", counts, cache._per_sequence)
-    _on_device(cache, fa_cache_keep, cache.args, lens, kept, counts, width, stream=stream)
+    cache._ints(lens=(lens, cache._per_sequence), kept=(kept, (cache.B, width)), counts=(counts, cache._per_sequence))
+    cache._call("fa_cache_keep", _pack_keep(lens.data_ptr(), kept.data_ptr(), counts.data_ptr(), width,
+                                            cache._raw_stream(stream)))
 
 
 def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scale=None, workspace=None, o=None,
@@ -649,35 +658,37 @@ def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scal
     [total, words] visibility bits (see ``tree_mask``).  ``max_new``: at least every sequence's number of
     new tokens.  ``o``, ``lse``, ``workspace``: tensors to use instead of new ones.  Returns (O, LSE),
     [total, Hq, d] and fp32 [total, Hq]."""
-    import torch
-    qs = cache._rows("q", q, None)
-    code = cache._type(q)
+    index = cache.index
+    if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache.Hk:
+        raise ValueError(f"expected q as [total, a multiple of {cache.Hk} heads, {cache.d}]")
     total, Hq, d = q.shape
-    cache._lengths("cu_new", cu_new, cache._bounds)
-    cache._lengths("lens", lens, cache._per_sequence)
-    words = 0
+    qt, qh = cache._rows("q", q, Hq)
+    code = cache._type(q)
+    cache._ints(cu_new=(cu_new, cache._bounds), lens=(lens, cache._per_sequence))
+    bits = words = 0
     if tree_mask is not None:
-        if not (tree_mask.get_device() == cache.index and tree_mask.dtype is torch.int64 and tree_mask.dim() == 2
+        if not (tree_mask.get_device() == index and tree_mask.dtype is _torch.int64 and tree_mask.dim() == 2
                 and tree_mask.is_contiguous() and tree_mask.shape[0] == total):
             raise ValueError("expected tree_mask as a contiguous int64 tensor [total, words] on the cache's device")
-        words = tree_mask.shape[1]
+        bits, words = tree_mask.data_ptr(), tree_mask.shape[1]
     if o is None:
-        o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif o.shape[0] != total or o.dtype is not q.dtype:
+        o = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif o.shape != q.shape or o.dtype is not q.dtype:
         raise ValueError("o and q differ in shape or type")
-    os_ = cache._rows("o", o, Hq)
+    ot, oh = cache._rows("o", o, Hq)
     if lse is None:
-        lse = torch.empty((total, Hq), dtype=torch.float32, device=q.device)
-    elif not (lse.get_device() == cache.index and lse.dtype is torch.float32 and lse.shape == (total, Hq)
+        lse = _torch.empty((total, Hq), dtype=_torch.float32, device=q.device)
+    elif not (lse.get_device() == index and lse.dtype is _torch.float32 and lse.shape == (total, Hq)
               and lse.is_contiguous()):
         raise ValueError("expected lse as a contiguous float32 tensor [total, Hq]")
     if workspace is None:
-        workspace = torch.empty(fa_fwd_tree_workspace_bytes(total, Hq, cache.Hk, d), dtype=torch.uint8, device=q.device)
-    elif not (workspace.get_device() == cache.index and workspace.is_contiguous()):
+        workspace = _torch.empty(fa_fwd_tree_workspace_bytes(total, Hq, cache.Hk, d), dtype=_torch.uint8, device=q.device)
+    elif not (workspace.get_device() == index and workspace.is_contiguous()):
         raise ValueError("expected workspace as a contiguous tensor on the cache's device")
-    _on_device(cache, fa_fwd_tree, cache.args, q, o, lse, qs, os_, cu_new, lens, tree_mask, words, total, Hq,
-               int(max_new), code, 1.0 / d ** 0.5 if scale is None else scale, workspace,
-               workspace.numel() * workspace.element_size(), stream=stream)
+    cache._call("fa_fwd_tree", _pack_tree(
+        q.data_ptr(), o.data_ptr(), lse.data_ptr(), qt, qh, ot, oh, cu_new.data_ptr(), lens.data_ptr(), bits,
+        words, total, Hq, max_new, code, 1.0 / d ** 0.5 if scale is None else scale, workspace.data_ptr(),
+        workspace.nbytes, cache._raw_stream(stream)))
     return o, lse
 
 

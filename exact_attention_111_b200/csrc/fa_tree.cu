@@ -640,18 +640,18 @@ __global__ void __launch_bounds__(384, 1)
 // Merge of the units cut between CTAs: block (c, y) takes rows of the unit that begins in CTA c and ends
 // in a later one.  With parts (m_i, l_i, O_i):
 //     O = sum_i 2^(m_i - m) O_i / sum_i 2^(m_i - m) l_i,  m = max_i m_i.
-// kSplit warps share a row's parts (few rows, up to 148 parts each) or each warp has its own row.
+// Few rows (up to 148 parts each): a block has one row, its eight warps share the parts.
 // ------------------------------------------------------------------------------------
-template <int D, bool kFp16, int kSplit>
+template <int D, bool kFp16>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   constexpr int kV = D / 32;                              // columns per lane
-  __shared__ float so[kSplit > 1 ? 8 : 1][D];
+  __shared__ float so[8][D];
   __shared__ float sl[8];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const int c = blockIdx.x, lane = lane_id(), warp = warp_id();
   const int4 me = a.meta[2 * c];                          // last CTA, rows, first token, key head
   const int row0 = a.meta[2 * c + 1].x;
-  const int r = kSplit > 1 ? blockIdx.y : blockIdx.y * 8 + warp, sub = kSplit > 1 ? warp : 0;
+  const int r = blockIdx.y;
   if (me.x < 0 || r >= me.y) return;
   const int n = me.x - c + 1;                             // parts: this CTA's and those of c + 1 .. me.x
   auto at = [&](int i) { return (2LL * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r; };
@@ -662,7 +662,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   const float neg = m == -INFINITY ? 0.f : -m;
   float l = 0.f, acc[kV] = {};
 #pragma unroll 4
-  for (int i = sub; i < n; i += kSplit) {
+  for (int i = warp; i < n; i += 8) {
     const long long k = at(i);
     const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + k * 2);
     const float w = ex2(ml.x + neg);
@@ -674,21 +674,19 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
       acc[j + 1] += w * x.y;
     }
   }
-  if constexpr (kSplit > 1) {
 #pragma unroll
-    for (int j = 0; j < kV; ++j) so[warp][lane * kV + j] = acc[j];
-    if (lane == 0) sl[warp] = l;
-    __syncthreads();
-    if (warp != 0) return;
-    l = 0.f;
+  for (int j = 0; j < kV; ++j) so[warp][lane * kV + j] = acc[j];
+  if (lane == 0) sl[warp] = l;
+  __syncthreads();
+  if (warp != 0) return;
+  l = 0.f;
 #pragma unroll
-    for (int j = 0; j < kV; ++j) acc[j] = 0.f;
+  for (int j = 0; j < kV; ++j) acc[j] = 0.f;
 #pragma unroll
-    for (int w = 0; w < 8; ++w) {
-      l += sl[w];
+  for (int w = 0; w < 8; ++w) {
+    l += sl[w];
 #pragma unroll
-      for (int j = 0; j < kV; ++j) acc[j] += so[w][lane * kV + j];
-    }
+    for (int j = 0; j < kV; ++j) acc[j] += so[w][lane * kV + j];
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
@@ -698,6 +696,43 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   uint32_t* op = reinterpret_cast<uint32_t*>(a.o + tk * a.o_tok + hq * a.o_head + lane * kV);
 #pragma unroll
   for (int j = 0; j < kV; j += 2) op[j / 2] = pack2<kFp16>(acc[j] * inv, acc[j + 1] * inv);
+}
+
+// Many rows (the tensor-memory kernel's slots: four columns of all rows, then the next four): a lane has a
+// row, a warp eight columns, a block 32 rows and 64 columns.
+template <int D, bool kFp16>
+__global__ void __launch_bounds__(256) tree_merge_rows_kernel(const TreeArgs a) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int c = blockIdx.x, lane = lane_id(), warp = warp_id();
+  const int4 me = a.meta[2 * c];                          // last CTA, rows, first token, key head
+  const int row0 = a.meta[2 * c + 1].x;
+  const int r = (blockIdx.y / (D / 64)) * 32 + lane, col = (blockIdx.y % (D / 64)) * 64 + warp * 8;
+  if (me.x < 0 || r >= me.y) return;
+  const int n = me.x - c + 1;                             // parts: this CTA's and those of c + 1 .. me.x
+  auto slot = [&](int i) { return 2LL * (c + i) + (i == 0 ? 1 : 0); };
+  float m = -INFINITY;
+  for (int i = 0; i < n; ++i) m = fmaxf(m, a.part_ml[(slot(i) * a.slot_rows + r) * 2]);
+  const float neg = m == -INFINITY ? 0.f : -m;
+  float l = 0.f, acc[8] = {};
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const long long k = slot(i);
+    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + (k * a.slot_rows + r) * 2);
+    const float w = ex2(ml.x + neg);
+    l += w * ml.y;
+    const float4* p = reinterpret_cast<const float4*>(a.part_o) + (k * (D / 4) + col / 4) * a.slot_rows + r;
+    const float4 x = p[0], y = p[a.slot_rows];
+    acc[0] += w * x.x; acc[1] += w * x.y; acc[2] += w * x.z; acc[3] += w * x.w;
+    acc[4] += w * y.x; acc[5] += w * y.y; acc[6] += w * y.z; acc[7] += w * y.w;
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
+  const long long tk = me.z + t;
+  const int hq = me.w * a.G + g;
+  if (col == 0) a.lse[tk * a.Hq + hq] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2f;
+  *reinterpret_cast<uint4*>(a.o + tk * a.o_tok + hq * a.o_head + col) =
+      make_uint4(pack2<kFp16>(acc[0] * inv, acc[1] * inv), pack2<kFp16>(acc[2] * inv, acc[3] * inv),
+                 pack2<kFp16>(acc[4] * inv, acc[5] * inv), pack2<kFp16>(acc[6] * inv, acc[7] * inv));
 }
 
 template <int D, bool kFp8, bool kFp16, int kNR>
@@ -739,8 +774,8 @@ cudaError_t launch_small_d(const CUtensorMap& tk, const CUtensorMap& tv, const T
 template <int D, bool kFp16>
 cudaError_t launch_merge_d(const TreeArgs& a, int ctas, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  const bool few = a.slot_rows <= 32;
-  cfg.gridDim = dim3(ctas, few ? a.slot_rows : (a.slot_rows + 7) / 8, 1);
+  const bool few = a.tile_rows < kBigRows;
+  cfg.gridDim = dim3(ctas, few ? a.slot_rows : (a.slot_rows + 31) / 32 * (D / 64), 1);
   cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -748,8 +783,8 @@ cudaError_t launch_merge_d(const TreeArgs& a, int ctas, cudaStream_t s) {
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kFp16, 8>, a)
-             : cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kFp16, 1>, a);
+  return few ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kFp16>, a)
+             : cudaLaunchKernelEx(&cfg, tree_merge_rows_kernel<D, kFp16>, a);
 }
 
 struct TreeLayout {

@@ -786,14 +786,15 @@ __global__ void __launch_bounds__(512, 1)
             dst[i] = w;
           }
         } else {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + ((long long)slot * a.slot_rows + r) * D + cc);
+          // four columns of all rows, then the next four: a warp's stores are contiguous
+          uint4* dst = reinterpret_cast<uint4*>(a.part_o) + ((long long)slot * (D / 4) + cc / 4) * a.slot_rows + r;
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
             if constexpr (kFp8) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) o[4 * i + k] = __float_as_uint(__uint_as_float(o[4 * i + k]) * inv);
             }
-            dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            dst[(long long)i * a.slot_rows] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
           }
         }
       }
