@@ -299,6 +299,24 @@ CacheView view_of(const fa_cache& c);
 void note_launches(int n);
 bool encode_cache(CUtensorMap* m, const void* base, long long rows, int d, int elem, int box_rows, bool all_panels);
 
+// Sets a kernel's dynamic shared memory once per device, and checks once that it was built with the registers
+// its setmaxnreg shares assume (the increase waits until the block's launch registers cover them).
+template <typename F>
+cudaError_t prepare_kernel(F* kern, int smem, int regs, bool (&done)[128]) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess || dev < 0 || dev >= 128) return e != cudaSuccess ? e : cudaErrorInvalidDevice;
+  if (done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes at;
+  e = cudaFuncGetAttributes(&at, kern);
+  if (e != cudaSuccess) return e;
+  if (at.numRegs != regs) return cudaErrorInvalidConfiguration;
+  done[dev] = true;              // two threads may both get here: the same is done twice
+  return cudaSuccess;
+}
+
 cudaError_t launch_tree_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp8, bool fp16,
                             int ctas, cudaStream_t s);
 

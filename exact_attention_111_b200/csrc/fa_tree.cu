@@ -739,18 +739,9 @@ template <int D, bool kFp8, bool kFp16, int kNR>
 cudaError_t launch_small(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, cudaStream_t s) {
   auto kern = tree_small_kernel<D, kFp8, kFp16, kNR>;
   constexpr int smem = SmallCfg<D, kFp8>::kSmem;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  static bool done[128];
+  const cudaError_t e = prepare_kernel(kern, smem, SmallCfg<D, kFp8>::kLaunchRegs, done);
   if (e != cudaSuccess) return e;
-  // setmaxnreg.inc waits until the block's launch registers cover every warpgroup's share: refuse a
-  // build whose register count differs from the one the shares assume.
-  static int regs = 0;
-  if (regs == 0) {
-    cudaFuncAttributes at;
-    const cudaError_t f = cudaFuncGetAttributes(&at, kern);
-    if (f != cudaSuccess) return f;
-    regs = at.numRegs;
-  }
-  if (regs != SmallCfg<D, kFp8>::kLaunchRegs) return cudaErrorInvalidConfiguration;
   kern<<<ctas, 384, smem, s>>>(tk, tv, a);
   return cudaGetLastError();
 }

@@ -443,7 +443,11 @@ __global__ void __launch_bounds__(512, 1)
       if (lane == 0) {
         const uint32_t idesc_s = idesc_f16(128, 128, kMmaFp16, false, false);
         const uint32_t idesc_pv = idesc_f16(128, D, kMmaFp16, false, true);
-        const uint32_t aQ = smem_addr(sQ), aK = smem_addr(sK), aV = smem_addr(sV);
+// Operand descriptors: the upper half is constant, the lower a sum in the address field (16-byte
+        // units).  (As 64-bit sums both halves go through registers: 167 -> 188 us at trees of 64.)
+        constexpr uint64_t kHi = (uint64_t)((1024 >> 4) | (1 << 14) | (2 << 29)) << 32;   // see smem_desc_sw128
+        const uint32_t lQ = (smem_addr(sQ) >> 4) | (16 >> 4) << 16, lK = (smem_addr(sK) >> 4) | (16 >> 4) << 16;
+        const uint32_t lV = (smem_addr(sV) >> 4) | (C::kPanelBytes >> 4) << 16;
         int nt = 0;                                       // tiles before this segment
         int np[2] = {0, 0};                               // P tiles consumed
         uint32_t tails = 0;                               // bit s: parity of stage s's safe V tiles
@@ -468,11 +472,11 @@ __global__ void __launch_bounds__(512, 1)
               if (!mbar_wait(&sh.p_full[q], np[q] & 1, abort_flag, st)) return false;
               if (!mbar_wait(&sh.o_ready[q], np[q] & 1, abort_flag, st)) return false;
               tc_fence_after();
+              const uint32_t lv = lV + (sp * C::kTileBytes >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kTile / 16; ++kk) {
-                const uint64_t bdesc = smem_desc_sw128(aV + sp * C::kTileBytes + kk * 2048, C::kPanelBytes, 1024);
-                mma_ts(tmem + C::kOCol + q * D, tmem + q * 128 + kk * 8, bdesc, idesc_pv, (u > 1 || kk > 0) ? 1u : 0u);
-              }
+              for (int kk = 0; kk < kTile / 16; ++kk)
+                mma_ts(tmem + C::kOCol + q * D, tmem + q * 128 + kk * 8, kHi | (lv + (kk * 2048 >> 4)), idesc_pv,
+                       (u > 1 || kk > 0) ? 1u : 0u);
               ++np[q];
               return true;
             };
@@ -487,12 +491,11 @@ __global__ void __launch_bounds__(512, 1)
                 ++nseg[q];
               }
               tc_fence_after();
+              const uint32_t lq = lQ + (q * C::kTileBytes >> 4), lk = lK + (sc * C::kTileBytes >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t koff = (kk >> 2) * C::kPanelBytes + (kk & 3) * 32;
-                const uint64_t adesc = smem_desc_sw128(aQ + q * C::kTileBytes + koff, 16, 1024);
-                const uint64_t bdesc = smem_desc_sw128(aK + sc * C::kTileBytes + koff, 16, 1024);
-                mma_ss(tmem + q * 128, adesc, bdesc, idesc_s, kk > 0 ? 1u : 0u);
+                const uint32_t koff = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
+                mma_ss(tmem + q * 128, kHi | (lq + koff), kHi | (lk + koff), idesc_s, kk > 0 ? 1u : 0u);
               }
               tc_commit(&sh.s_full[q]);
               return true;
@@ -814,18 +817,9 @@ template <int D, bool kFp8, bool kFp16>
 cudaError_t launch_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, cudaStream_t s) {
   using C = BigCfg<D, kFp8>;
   auto kern = tree_big_kernel<D, kFp8, kFp16>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static bool done[128];
+  const cudaError_t e = prepare_kernel(kern, C::kSmem, C::kLaunchRegs, done);
   if (e != cudaSuccess) return e;
-  // setmaxnreg.inc waits until the block's launch registers cover every warpgroup's share: refuse a
-  // build whose register count differs from the one the shares assume.
-  static int regs = 0;
-  if (regs == 0) {
-    cudaFuncAttributes at;
-    e = cudaFuncGetAttributes(&at, kern);
-    if (e != cudaSuccess) return e;
-    regs = at.numRegs;
-  }
-  if (regs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
   kern<<<ctas, 512, C::kSmem, s>>>(tk, tv, a);
   return cudaGetLastError();
 }
