@@ -270,6 +270,13 @@ __device__ void stage_role(const TreeArgs& a, BigShared& sh, uint8_t* sC, const 
   __syncwarp();
 }
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // Warps 14 and 15 with an E4M3 cache: K into the ring, and each tile's factors.
 template <int D, int kStages>
 __device__ void expand_k_role(const TreeArgs& a, BigShared& sh, uint8_t* sK, const uint8_t* sC, Walk& w, int wi) {
@@ -440,75 +447,87 @@ __global__ void __launch_bounds__(512, 1)
       __syncwarp();
     } else if (warp == C::kMmaWarp) {
       // ---------------------------------------------------------------- MMA issuer
-      if (lane == 0) {
-        const uint32_t idesc_s = idesc_f16(128, 128, kMmaFp16, false, false);
-        const uint32_t idesc_pv = idesc_f16(128, D, kMmaFp16, false, true);
-// Operand descriptors: the upper half is constant, the lower a sum in the address field (16-byte
-        // units).  (As 64-bit sums both halves go through registers: 167 -> 188 us at trees of 64.)
-        constexpr uint64_t kHi = (uint64_t)((1024 >> 4) | (1 << 14) | (2 << 29)) << 32;   // see smem_desc_sw128
-        const uint32_t lQ = (smem_addr(sQ) >> 4) | (16 >> 4) << 16, lK = (smem_addr(sK) >> 4) | (16 >> 4) << 16;
-        const uint32_t lV = (smem_addr(sV) >> 4) | (C::kPanelBytes >> 4) << 16;
-        int nt = 0;                                       // tiles before this segment
-        int np[2] = {0, 0};                               // P tiles consumed
-        uint32_t tails = 0;                               // bit s: parity of stage s's safe V tiles
-        uint32_t nseg[2] = {0, 0};
-        bool ok = true;
-        while (ok && w.next(a)) {
-          const int nq = e.nrows > kTile ? 2 : 1;
-          for (int u = 0; u <= e.nu && ok && e.nu > 0; ++u) {
-            const int tp = nt + u - 1, tc = nt + u;
-            const int sp = (tp + C::kStages) % C::kStages, sc = tc % C::kStages;
-            bool v_ready = false, k_ready = false;
-            auto pv = [&](int q) -> bool {
-              if (u == 0 || q >= nq) return true;
-              if (!v_ready) {
-                if (!mbar_wait(&sh.v_full[sp], (tp / C::kStages) & 1, abort_flag, st)) return false;
-                if (!kFp8 && tail_tile(e, e.kt0 + u - 1)) {
-                  if (!mbar_wait(&sh.v_ok[sp], (tails >> sp) & 1u, abort_flag, st)) return false;
-                  tails ^= 1u << sp;
-                }
-                v_ready = true;
+      // The whole warp walks and waits, one elected lane issues: the operands are then the same in all
+      // lanes, broadcast so that the compiler knows, and stay in uniform registers.
+      const bool leader = elect_one();
+      const uint32_t idesc_s = idesc_f16(128, 128, kMmaFp16, false, false);
+      const uint32_t idesc_pv = idesc_f16(128, D, kMmaFp16, false, true);
+      // Operand descriptors: the upper half is constant, the lower a sum in the address field (16-byte
+      // units).  (As 64-bit sums both halves go through registers: 167 -> 188 us at trees of 64.)
+      constexpr uint64_t kHi = (uint64_t)((1024 >> 4) | (1 << 14) | (2 << 29)) << 32;   // see smem_desc_sw128
+      const uint32_t lQ = (smem_addr(sQ) >> 4) | (16 >> 4) << 16, lK = (smem_addr(sK) >> 4) | (16 >> 4) << 16;
+      const uint32_t lV = (smem_addr(sV) >> 4) | (C::kPanelBytes >> 4) << 16;
+      const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+      int nt = 0;                                         // tiles before this segment
+      int np[2] = {0, 0};                                 // P tiles consumed
+      uint32_t tails = 0;                                 // bit s: parity of stage s's safe V tiles
+      uint32_t nseg[2] = {0, 0};
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return (bool)__all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, st));
+      };
+      while (ok && w.next(a)) {
+        const int nq = e.nrows > kTile ? 2 : 1;
+        for (int u = 0; u <= e.nu && ok && e.nu > 0; ++u) {
+          const int tp = nt + u - 1, tc = nt + u;
+          const int sp = (tp + C::kStages) % C::kStages, sc = tc % C::kStages;
+          bool v_ready = false, k_ready = false;
+          auto pv = [&](int q) -> bool {
+            if (u == 0 || q >= nq) return true;
+            if (!v_ready) {
+              if (!wait(&sh.v_full[sp], (tp / C::kStages) & 1)) return false;
+              if (!kFp8 && tail_tile(e, e.kt0 + u - 1)) {
+                if (!wait(&sh.v_ok[sp], (tails >> sp) & 1u)) return false;
+                tails ^= 1u << sp;
               }
-              if (!mbar_wait(&sh.p_full[q], np[q] & 1, abort_flag, st)) return false;
-              if (!mbar_wait(&sh.o_ready[q], np[q] & 1, abort_flag, st)) return false;
-              tc_fence_after();
-              const uint32_t lv = lV + (sp * C::kTileBytes >> 4);
+              v_ready = true;
+            }
+            const uint32_t lv = __shfl_sync(0xffffffffu, lV + (sp * C::kTileBytes >> 4), 0);
+            const uint32_t more = __shfl_sync(0xffffffffu, u > 1 ? 1u : 0u, 0);
+            if (!wait(&sh.p_full[q], np[q] & 1) || !wait(&sh.o_ready[q], np[q] & 1)) return false;
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
-                mma_ts(tmem + C::kOCol + q * D, tmem + q * 128 + kk * 8, kHi | (lv + (kk * 2048 >> 4)), idesc_pv,
-                       (u > 1 || kk > 0) ? 1u : 0u);
-              ++np[q];
-              return true;
-            };
-            auto sq = [&](int q) -> bool {
-              if (u == e.nu || q >= nq) return true;
-              if (!k_ready) {
-                if (!mbar_wait(&sh.k_full[sc], (tc / C::kStages) & 1, abort_flag, st)) return false;
-                k_ready = true;
-              }
-              if (u == 0) {
-                if (!mbar_wait(&sh.q_full[q], nseg[q] & 1, abort_flag, st)) return false;
-                ++nseg[q];
-              }
-              tc_fence_after();
-              const uint32_t lq = lQ + (q * C::kTileBytes >> 4), lk = lK + (sc * C::kTileBytes >> 4);
+                mma_ts(tm + C::kOCol + q * D, tm + q * 128 + kk * 8, kHi | (lv + (kk * 2048 >> 4)), idesc_pv,
+                       kk > 0 ? 1u : more);
+            }
+            ++np[q];
+            return true;
+          };
+          auto sq = [&](int q) -> bool {
+            if (u == e.nu || q >= nq) return true;
+            if (!k_ready) {
+              if (!wait(&sh.k_full[sc], (tc / C::kStages) & 1)) return false;
+              k_ready = true;
+            }
+            if (u == 0) {
+              if (!wait(&sh.q_full[q], nseg[q] & 1)) return false;
+              ++nseg[q];
+            }
+            const uint32_t lk = __shfl_sync(0xffffffffu, lK + (sc * C::kTileBytes >> 4), 0);
+            const uint32_t lq = __shfl_sync(0xffffffffu, lQ + (q * C::kTileBytes >> 4), 0);
+            tc_fence_after();
+            if (leader) {
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint32_t koff = ((kk >> 2) * C::kPanelBytes + (kk & 3) * 32) >> 4;
-                mma_ss(tmem + q * 128, kHi | (lq + koff), kHi | (lk + koff), idesc_s, kk > 0 ? 1u : 0u);
+                mma_ss(tm + q * 128, kHi | (lq + koff), kHi | (lk + koff), idesc_s, kk > 0 ? 1u : 0u);
               }
               tc_commit(&sh.s_full[q]);
-              return true;
-            };
-            ok = pv(0) && sq(0) && pv(1);
-            if (u > 0 && ok) tc_commit(&sh.v_empty[sp]);
-            ok = ok && sq(1);
-            if (u < e.nu && ok) tc_commit(&sh.k_empty[sc]);
-          }
-          nt += e.nu;
-          if (ok && e.nu > 0)
-            for (int q = 0; q < nq; ++q) tc_commit(&sh.o_full[q]);   // O_q holds every product
+            }
+            return true;
+          };
+          ok = pv(0) && sq(0) && pv(1);
+          if (u > 0 && ok && leader) tc_commit(&sh.v_empty[sp]);
+          ok = ok && sq(1);
+          if (u < e.nu && ok && leader) tc_commit(&sh.k_empty[sc]);
         }
+        nt += e.nu;
+        if (ok && e.nu > 0 && leader)
+          for (int q = 0; q < nq; ++q) tc_commit(&sh.o_full[q]);   // O_q holds every product
+      }
+      if (leader) {
         tc_commit(&sh.mma_done);
         mbar_wait_drain(&sh.mma_done, 0, st);
       }
