@@ -317,6 +317,28 @@ cudaError_t prepare_kernel(F* kern, int smem, int regs, bool (&done)[128]) {
   return cudaSuccess;
 }
 
+// The attention's kernels may be brought onto the SMs while the kernel before them in the stream still runs:
+// they are launched so, set up their barriers, and in grid_begin wait for that kernel's end and for its
+// writes to be visible, before the first access to global memory; then they let the next one come.
+__device__ __forceinline__ void grid_begin() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+template <typename... A, typename... B>
+cudaError_t launch_after(void (*kern)(A...), dim3 grid, int threads, size_t smem, cudaStream_t s, const B&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads, 1, 1);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<A>(args)...);
+}
+
 cudaError_t launch_tree_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, bool fp8, bool fp16,
                             int ctas, cudaStream_t s);
 

@@ -149,16 +149,14 @@ __global__ void __launch_bounds__(384, 1)
   volatile int* abort_flag = reinterpret_cast<int*>(empty + C::kStages);
   const DevStatus st{a.c.status, a.timeout_ns};
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x < C::kStages) {
     mbar_init(&full[threadIdx.x], kFp8 ? 2 + 2 * C::kChunkKeys / 16 : 2);         // both loaders, and their lanes that copy codes
     mbar_init(&empty[threadIdx.x], 8);
   }
-  if (threadIdx.x == 0) {
-    *abort_flag = 0;
-    a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
-  }
+  if (threadIdx.x == 0) *abort_flag = 0;
   fence_barrier_init();
+  grid_begin();
+  if (threadIdx.x == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   const Part part = find_part(a, blockIdx.x == 0 && warp == 0);
   if (part.n == 0) return;
   __syncthreads();
@@ -647,7 +645,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   constexpr int kV = D / 32;                              // columns per lane
   __shared__ float so[8][D];
   __shared__ float sl[8];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_begin();
   const int c = blockIdx.x, lane = lane_id(), warp = warp_id();
   const int4 me = a.meta[2 * c];                          // last CTA, rows, first token, key head
   const int row0 = a.meta[2 * c + 1].x;
@@ -702,7 +700,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
 // row, a warp eight columns, a block 32 rows and 64 columns.
 template <int D, bool kFp16>
 __global__ void __launch_bounds__(256) tree_merge_rows_kernel(const TreeArgs a) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_begin();
   const int c = blockIdx.x, lane = lane_id(), warp = warp_id();
   const int4 me = a.meta[2 * c];                          // last CTA, rows, first token, key head
   const int row0 = a.meta[2 * c + 1].x;
@@ -742,8 +740,7 @@ cudaError_t launch_small(const CUtensorMap& tk, const CUtensorMap& tv, const Tre
   static bool done[128];
   const cudaError_t e = prepare_kernel(kern, smem, SmallCfg<D, kFp8>::kLaunchRegs, done);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, 384, smem, s>>>(tk, tv, a);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(ctas), 384, smem, s, tk, tv, a);
 }
 
 template <int D, bool kFp8, bool kFp16>
@@ -760,22 +757,11 @@ cudaError_t launch_small_d(const CUtensorMap& tk, const CUtensorMap& tv, const T
   return fp16 ? launch_small_nr<D, false, true>(tk, tv, a, ctas, s) : launch_small_nr<D, false, false>(tk, tv, a, ctas, s);
 }
 
-// Launched so that its blocks may start while the attention kernel still runs (they wait for its
-// end on the device): saves most of a launch's latency.
 template <int D, bool kFp16>
 cudaError_t launch_merge_d(const TreeArgs& a, int ctas, cudaStream_t s) {
-  cudaLaunchConfig_t cfg{};
-  const bool few = a.tile_rows < kBigRows;
-  cfg.gridDim = dim3(ctas, few ? a.slot_rows : (a.slot_rows + 31) / 32 * (D / 64), 1);
-  cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return few ? cudaLaunchKernelEx(&cfg, tree_merge_kernel<D, kFp16>, a)
-             : cudaLaunchKernelEx(&cfg, tree_merge_rows_kernel<D, kFp16>, a);
+  if (a.tile_rows < kBigRows)
+    return launch_after(tree_merge_kernel<D, kFp16>, dim3(ctas, a.slot_rows), 256, 0, s, a);
+  return launch_after(tree_merge_rows_kernel<D, kFp16>, dim3(ctas, (a.slot_rows + 31) / 32 * (D / 64)), 256, 0, s, a);
 }
 
 struct TreeLayout {

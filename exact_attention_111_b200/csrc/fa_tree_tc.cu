@@ -140,10 +140,11 @@ __device__ __forceinline__ uint32_t next_eref(uint32_t eref, uint32_t ev, bool f
 
 // Expand one tile (128 rows of D codes, as TMA staged them) into a ring tile: warp wi of nW.  A pass
 // of a warp is 32 / kLanes rows; row factors are computed once, two or one per lane, and
-// shuffled.  clean (V): rows from `keys` on become zero and NaN codes too; returns whether there were.
+// shuffled.  `read` is arrived on once the codes are in registers.  clean (V): rows from `keys` on become
+// zero and NaN codes too; returns whether there were.
 template <int D, int nW>
 __device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, const uint8_t* scales, int e, int wi,
-                                            bool clean, int keys) {
+                                            uint64_t* read, bool clean, int keys) {
   constexpr int kLanes = D / 16, kW = 32 / kLanes, kF = kTile / nW / 32, kPasses = kTile / (nW * kW);
   const int lane = lane_id();
   const int chunk = lane % kLanes, sub = lane / kLanes;
@@ -159,22 +160,23 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, 
   const int r0 = wi * kW + sub;
   const int c0 = (2 * chunk) & 7, sw = D == 128 ? (chunk >> 2) & 1 : 0;
   uint8_t* dst = dst0 + (chunk >> 2) * (kTile * 128);
-  static_assert(kPasses % 4 == 0, "passes");
+  static_assert(kPasses % 2 == 0, "passes");
 #pragma unroll 1
-  for (int i0 = 0; i0 < kPasses; i0 += 4) {               // four passes' loads in flight
-    uint2 x[4][2];
-    uint32_t fi[4];
+  for (int i0 = 0; i0 < kPasses; i0 += 2) {               // two passes in flight (four: 5 % slower, spills)
+    uint2 x[2][2];
+    uint32_t fi[2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int p = i0 + i, r = r0 + p * nW * kW;
       const uint8_t* src = src0 + (D == 64 ? r * 64 + ((chunk ^ ((r >> 1) & 3)) << 4) : r * 128 + ((chunk ^ (r & 7)) << 4));
       x[i][0] = *reinterpret_cast<const uint2*>(src + 8 * sw);
       x[i][1] = *reinterpret_cast<const uint2*>(src + 8 - 8 * sw);
       fi[i] = __shfl_sync(0xffffffffu, kF > 1 && p * kW >= 32 ? f[kF - 1] : f[0], (p * kW) % 32 + sub);
     }
+    if (i0 + 2 == kPasses) mbar_arrive(read);
     if (clean) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 2; ++i) {
         const bool past = r0 + (i0 + i) * nW * kW >= keys;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -189,7 +191,7 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, 
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 2; ++i) {
       const int r = r0 + (i0 + i) * nW * kW;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
@@ -303,10 +305,9 @@ __device__ void expand_k_role(const TreeArgs& a, BigShared& sh, uint8_t* sK, con
         *reinterpret_cast<volatile float*>(&sh.vref[n & 7]) = scale_value(en);
       }
       eref = en;
-      expand_tile<D, 2>(sC, sK + s * (kTile * D * 2), sh.scales[0], (int)ek, wi, false, 0);
+      expand_tile<D, 2>(sC, sK + s * (kTile * D * 2), sh.scales[0], (int)ek, wi, &sh.c_empty[0], false, 0);
       fence_async_smem();
       mbar_arrive(&sh.k_full[s]);
-      mbar_arrive(&sh.c_empty[0]);
     }
   }
 }
@@ -351,7 +352,6 @@ __global__ void __launch_bounds__(512, 1)
   const DevStatus st{a.c.status, a.timeout_ns};
   volatile int* abort_flag = &sh.abort_flag;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&sh.k_full[s], kFp8 ? 64 : 1);
@@ -381,6 +381,7 @@ __global__ void __launch_bounds__(512, 1)
     tmem_alloc(&sh.tmem_base, 512);
     tmem_relinquish();
   }
+  grid_begin();
   const Part part = find_part(a, blockIdx.x == 0 && warp == 0);
   if (threadIdx.x == 0) a.meta[2 * blockIdx.x] = make_int4(-1, 0, 0, 0);
   tc_fence_before();
@@ -555,12 +556,11 @@ __global__ void __launch_bounds__(512, 1)
         if (!__all_sync(0xffffffffu, go)) return false;
         const int keys = e.s.len + e.s.T - (e.kt0 + u) * kChunk;
         eref = next_eref(eref, top_scale(sh.scales[2], keys), u == 0);
-        if (expand_tile<D, 4>(sC + C::kCodes, sV + s * C::kTileBytes, sh.scales[2], (int)eref, wq,
+        if (expand_tile<D, 4>(sC + C::kCodes, sV + s * C::kTileBytes, sh.scales[2], (int)eref, wq, &sh.c_empty[1],
                               tail_tile(e, e.kt0 + u), keys))
           for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 7]) = seg[q] + 1;
         fence_async_smem();
         mbar_arrive(&sh.v_full[s]);
-        mbar_arrive(&sh.c_empty[1]);
         return true;
       };
       if constexpr (kFp8) {
@@ -839,8 +839,7 @@ cudaError_t launch_big(const CUtensorMap& tk, const CUtensorMap& tv, const TreeA
   static bool done[128];
   const cudaError_t e = prepare_kernel(kern, C::kSmem, C::kLaunchRegs, done);
   if (e != cudaSuccess) return e;
-  kern<<<ctas, 512, C::kSmem, s>>>(tk, tv, a);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(ctas), 512, C::kSmem, s, tk, tv, a);
 }
 
 template <int D>
