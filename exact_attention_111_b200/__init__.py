@@ -610,8 +610,8 @@ def cache_append(cache, k_new, v_new, cu_new, lens, stream=None):
     lens[b] + i of sequence b.  ``lens`` is not changed.  An E4M3 cache quantises them."""
     kt, kh = cache._rows("k_new", k_new, cache.Hk)
     vt, vh = cache._rows("v_new", v_new, cache.Hk)
-    total = len(k_new)
-    if len(v_new) != total or v_new.dtype is not k_new.dtype:
+    total = k_new.shape[0]
+    if v_new.shape[0] != total or v_new.dtype is not k_new.dtype:
         raise ValueError("k_new and v_new differ in shape or type")
     cache._ints(cu_new=(cu_new, cache._bounds), lens=(lens, cache._per_sequence))
     cache._call("fa_cache_append", _pack_append(

@@ -83,6 +83,7 @@ __device__ __forceinline__ uint2 quantise8(const uint4& w, int& code) {
 template <int D, bool kFp8, bool kFp16, int kSteps>
 __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
   constexpr int kLanes = D / 8, kHeads = 32 / kLanes;
+  grid_begin();
   const int lane = lane_id();
   const long long w = (long long)blockIdx.x * 8 + warp_id();
   const int tok = (int)(w / a.groups);
@@ -131,9 +132,9 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
 }
 
 template <int D, bool kFp8, bool kFp16>
-void launch_append(const AppendArgs& a, unsigned blocks, int steps, cudaStream_t s) {
-  if (steps == 4) append_kernel<D, kFp8, kFp16, 4><<<blocks, 256, 0, s>>>(a);
-  else append_kernel<D, kFp8, kFp16, 1><<<blocks, 256, 0, s>>>(a);
+cudaError_t launch_append(const AppendArgs& a, unsigned blocks, int steps, cudaStream_t s) {
+  return steps == 4 ? launch_after(append_kernel<D, kFp8, kFp16, 4>, dim3(blocks), 256, 0, s, a)
+                    : launch_after(append_kernel<D, kFp8, kFp16, 1>, dim3(blocks), 256, 0, s, a);
 }
 
 // ------------------------------------------------------------------------------------
@@ -166,6 +167,7 @@ constexpr int kReadRows = 64;
 template <int D, bool kFp8, bool kFp16>
 __global__ void __launch_bounds__(256) read_kernel(const ReadArgs a) {
   constexpr int kLanes = D / 8, kPass = 256 / kLanes;      // rows per pass of the block
+  grid_begin();
   const int tile = blockIdx.x % a.tiles;
   const int bh = blockIdx.x / a.tiles;
   const int b = bh / a.c.Hk, h = bh - b * a.c.Hk;
@@ -216,6 +218,7 @@ struct KeepArgs {
 template <int kRowBytes, bool kFp8>
 __global__ void __launch_bounds__(128) keep_kernel(const KeepArgs a) {
   constexpr int kLanes = kRowBytes / 16, kRows = 32 / kLanes;
+  grid_begin();
   const int lane = lane_id();
   const long long w = (long long)blockIdx.x * 4 + warp_id();
   const long long bh = w >> 1;
@@ -261,8 +264,7 @@ __global__ void __launch_bounds__(128) keep_kernel(const KeepArgs a) {
 
 template <typename F>
 int launched(F&& f) {
-  f();
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+  return f() == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 // Strides of a [tokens, heads, d] view: 16-byte rows, and no overlap is asked of the caller.
@@ -343,15 +345,15 @@ int fa_cache_append(const fa_cache_append_args* p) {
   const cudaStream_t s = static_cast<cudaStream_t>(x.stream);
   const bool fp8 = x.cache.dtype == FA_E4M3, fp16 = x.dtype == FA_FP16;
   const unsigned g = (unsigned)blocks;
-  return launched([&] {
+  return launched([&]() -> cudaError_t {
     if (x.cache.d == 128) {
-      if (!fp8) launch_append<128, false, false>(a, g, steps, s);
-      else if (fp16) launch_append<128, true, true>(a, g, steps, s);
-      else launch_append<128, true, false>(a, g, steps, s);
+      if (!fp8) return launch_append<128, false, false>(a, g, steps, s);
+      else if (fp16) return launch_append<128, true, true>(a, g, steps, s);
+      else return launch_append<128, true, false>(a, g, steps, s);
     } else {
-      if (!fp8) launch_append<64, false, false>(a, g, steps, s);
-      else if (fp16) launch_append<64, true, true>(a, g, steps, s);
-      else launch_append<64, true, false>(a, g, steps, s);
+      if (!fp8) return launch_append<64, false, false>(a, g, steps, s);
+      else if (fp16) return launch_append<64, true, true>(a, g, steps, s);
+      else return launch_append<64, true, false>(a, g, steps, s);
     }
   });
 }
@@ -379,15 +381,15 @@ int fa_cache_read(const fa_cache_read_args* p) {
   const cudaStream_t s = static_cast<cudaStream_t>(x.stream);
   const bool fp8 = x.cache.dtype == FA_E4M3, fp16 = x.dtype == FA_FP16;
   const unsigned g = (unsigned)blocks;
-  return launched([&] {
+  return launched([&]() -> cudaError_t {
     if (x.cache.d == 128) {
-      if (!fp8) read_kernel<128, false, false><<<g, 256, 0, s>>>(a);
-      else if (fp16) read_kernel<128, true, true><<<g, 256, 0, s>>>(a);
-      else read_kernel<128, true, false><<<g, 256, 0, s>>>(a);
+      if (!fp8) return launch_after(read_kernel<128, false, false>, dim3(g), 256, 0, s, a);
+      else if (fp16) return launch_after(read_kernel<128, true, true>, dim3(g), 256, 0, s, a);
+      else return launch_after(read_kernel<128, true, false>, dim3(g), 256, 0, s, a);
     } else {
-      if (!fp8) read_kernel<64, false, false><<<g, 256, 0, s>>>(a);
-      else if (fp16) read_kernel<64, true, true><<<g, 256, 0, s>>>(a);
-      else read_kernel<64, true, false><<<g, 256, 0, s>>>(a);
+      if (!fp8) return launch_after(read_kernel<64, false, false>, dim3(g), 256, 0, s, a);
+      else if (fp16) return launch_after(read_kernel<64, true, true>, dim3(g), 256, 0, s, a);
+      else return launch_after(read_kernel<64, true, false>, dim3(g), 256, 0, s, a);
     }
   });
 }
@@ -412,13 +414,13 @@ int fa_cache_keep(const fa_cache_keep_args* p) {
   a.width = x.width;
   const cudaStream_t s = static_cast<cudaStream_t>(x.stream);
   const unsigned g = (unsigned)blocks;
-  return launched([&] {
+  return launched([&]() -> cudaError_t {
     if (x.cache.dtype == FA_E4M3) {
-      if (x.cache.d == 128) keep_kernel<128, true><<<g, 128, 0, s>>>(a);
-      else keep_kernel<64, true><<<g, 128, 0, s>>>(a);
+      if (x.cache.d == 128) return launch_after(keep_kernel<128, true>, dim3(g), 128, 0, s, a);
+      else return launch_after(keep_kernel<64, true>, dim3(g), 128, 0, s, a);
     } else {
-      if (x.cache.d == 128) keep_kernel<256, false><<<g, 128, 0, s>>>(a);
-      else keep_kernel<128, false><<<g, 128, 0, s>>>(a);
+      if (x.cache.d == 128) return launch_after(keep_kernel<256, false>, dim3(g), 128, 0, s, a);
+      else return launch_after(keep_kernel<128, false>, dim3(g), 128, 0, s, a);
     }
   });
 }

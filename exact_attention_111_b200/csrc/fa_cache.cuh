@@ -317,7 +317,7 @@ cudaError_t prepare_kernel(F* kern, int smem, int regs, bool (&done)[128]) {
   return cudaSuccess;
 }
 
-// The attention's kernels may be brought onto the SMs while the kernel before them in the stream still runs:
+// The cache's and the attention's kernels may be brought onto the SMs while the kernel before them in the stream still runs:
 // they are launched so, set up their barriers, and in grid_begin wait for that kernel's end and for its
 // writes to be visible, before the first access to global memory; then they let the next one come.
 __device__ __forceinline__ void grid_begin() {
