@@ -699,7 +699,8 @@ def tree_mask(parents, cu_new, words=None):
     it); ``cu_new`` as for attention_forward_tree.  Computed on the host (trees are
     drafted there or are fixed); the result is on ``cu_new``'s device."""
     import torch
-    par, cu = [int(x) for x in parents], [int(x) for x in cu_new]
+    par = parents.tolist() if isinstance(parents, torch.Tensor) else [int(x) for x in parents]
+    cu = cu_new.tolist()
     most = max([b - a for a, b in zip(cu, cu[1:])] + [1])
     words = (most + 63) // 64 if words is None else words
     if 64 * words < most:

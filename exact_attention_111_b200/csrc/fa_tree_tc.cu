@@ -14,9 +14,9 @@
 // a finished S_q(u) also says that O_q holds every earlier product.
 //
 // A masked product is 0 * v, which is not 0 where v is not finite.  Tiles that hold new tokens (which some
-// rows see and others do not) or lie past the end are therefore read once more by the correction
+// rows see and others do not) or reach past the end are therefore read once more by the correction
 // warps before their product: rows past the sequence's end become zero, and values that are not
-// finite do too, noted; the epilogue then adds those to the rows that see them.
+// finite do too, noted; the epilogue then adds those of such tiles to the rows that see them.
 #include <climits>
 
 #include "fa.h"
@@ -93,9 +93,10 @@ struct BigShared {
   uint64_t mma_done;
   uint32_t tmem_base;
   int abort_flag;
-  // [group][its segments mod 8]: number + 1 of a segment where a new token's value was not finite.  Who
-  // writes them is at most kStages + 1 tiles, so 5 segments, ahead of the slower softmax group.
-  int odd[2][8];
+  // [group][its segments mod 2]: number + 1 of a segment with a value that was made safe.  The correction
+  // warps reach a group's segment n + 2 only with all its alphas of segment n + 1, which it
+  // publishes after it has read entry n.
+  int odd[2][2];
   float alpha[2][kTile];
   // E4M3: staged scale codes of a tile (K's and V's with K, V's with V), and by tile mod 8 the factors of its K, of what O
   // holds and of O.  Entry u is written again for tile u + 8, whose K slot is free only
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(512, 1)
       mbar_init(&sh.p_full[q], 128);
       mbar_init(&sh.alpha_full[q], 128);
       mbar_init(&sh.o_ready[q], 128);
-      for (int i = 0; i < 8; ++i) sh.odd[q][i] = 0;
+      sh.odd[q][0] = sh.odd[q][1] = 0;
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.c_full[i], 1);
@@ -558,7 +559,7 @@ __global__ void __launch_bounds__(512, 1)
         eref = next_eref(eref, top_scale(sh.scales[2], keys), u == 0);
         if (expand_tile<D, 4>(sC + C::kCodes, sV + s * C::kTileBytes, sh.scales[2], (int)eref, wq, &sh.c_empty[1],
                               tail_tile(e, e.kt0 + u), keys))
-          for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 7]) = seg[q] + 1;
+          for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 1]) = seg[q] + 1;
         fence_async_smem();
         mbar_arrive(&sh.v_full[s]);
         return true;
@@ -590,7 +591,7 @@ __global__ void __launch_bounds__(512, 1)
             if (odd) {
               *p = x;
               if (!past)
-                for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 7]) = seg[q] + 1;
+                for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 1]) = seg[q] + 1;
             }
           }
           fence_async_smem();
@@ -755,7 +756,7 @@ __global__ void __launch_bounds__(512, 1)
         a.meta[2 * blockIdx.x] = make_int4(part.line.owner(e.g + e.s.KT - 1), e.nrows, e.s.cu0, e.h);
         a.meta[2 * blockIdx.x + 1] = make_int4(e.row0, 0, 0, 0);
       }
-      const bool odd = e.nu > 0 && *reinterpret_cast<volatile int*>(&sh.odd[q][(nseg - 1) & 7]) == nseg;
+      const bool odd = e.nu > 0 && *reinterpret_cast<volatile int*>(&sh.odd[q][(nseg - 1) & 1]) == nseg;
       const float inv = whole ? (l == 0.f ? 0.f : vref / l) : vref;
       const int hq = e.h * a.G + (R - t * a.G);
       const long long tk = e.s.cu0 + t;
@@ -779,8 +780,9 @@ __global__ void __launch_bounds__(512, 1)
         }
         if (!live) continue;
         if (odd) {                                        // rare: see the top of the file
+          // keys of the segment's tiles that were made safe; j < 0 is the prefix
           const int j1 = min(e.s.T, (e.kt0 + e.nu) * kChunk - e.s.len);
-          for (int j = max(0, e.kt0 * kChunk - e.s.len); j < j1; ++j) {
+          for (int j = max(e.kt0, e.s.len / kChunk) * kChunk - e.s.len; j < j1; ++j) {
             if (!(visible32(a, e.s, t, j) & 1u)) continue;
             const long long row = slot_row(a.c, e.b, e.h, (long long)e.s.len + j);
             if (row < 0) continue;

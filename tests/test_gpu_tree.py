@@ -125,6 +125,56 @@ def test_nan_codes_of_the_prefix(dtype, n):
     assert torch.isnan(o[:, :2, 17]).all() and torch.isnan(o[:, 2:]).all()
 
 
+@pytest.mark.parametrize("mask", ["chain", "random"])
+@pytest.mark.parametrize("n", [3, 40, 300])
+@pytest.mark.parametrize("dtype,fp8", [(BF, False), (HF, False), (BF, True), (HF, True)])
+def test_values_of_the_prefix_beside_new_tokens(dtype, fp8, n, mask):
+    """Prefix keys in the same block of keys as the first new tokens: NaN and infinities there reach
+    every row, also where the block's masked products are made safe."""
+    c = Case([200], [n], 2, 64, 16, dtype, fp8, seed=n)
+    c.put(c.new(2), c.new(2))
+    for pos, col, x in ((199, 5, float("nan")), (193, 9, float("inf")), (140, 40, -float("inf"))):
+        p, r = c.table_np[0, pos // 16], pos % 16
+        c.gpu["v"][p, 1, r, col] = 127 if fp8 else x
+    q = c.new(4).cuda()
+    bits = _masks(mask, c, seed=1)
+    o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, n, tree_mask=bits)
+    fa.fa_check_status()
+    check_attention(c, q, o, lse, 1 / 8, bits, nan_ok=True)
+    assert not torch.isfinite(o[:, 2:, [5, 9, 40]]).any()
+
+
+def test_rows_behind_four_gigabytes():
+    """A cache whose K and V are over 4 GB each: positions in its last pages."""
+    pages, Hk, page, d = 40000, 8, 64, 128
+    k = torch.empty(pages, Hk, page, d, dtype=BF, device="cuda")
+    v = torch.empty_like(k)
+    assert k.numel() * 2 > 2 ** 32
+    g = torch.Generator().manual_seed(2)
+    small = Case([150], [3], Hk, d, page, BF, False, seed=3)          # the same sequence in a small cache
+    big_table = torch.tensor([[pages - 1, pages - 5, pages - 2, 0]], dtype=torch.int32, device="cuda")
+    for e in range(3):
+        k[big_table[0, e]] = small.gpu["k"][small.table_np[0, e]]
+        v[big_table[0, e]] = small.gpu["v"][small.table_np[0, e]]
+    big = fa.KVCache(k, v, big_table)
+    kn, vn = (torch.randn(3, Hk, d, generator=g).to(BF).cuda() for _ in range(2))
+    q = torch.randn(3, 16, d, generator=g).to(BF).cuda()
+    one = torch.tensor([0, 1, 3], dtype=torch.int32, device="cuda")[None, 1:].contiguous()
+    two = torch.tensor([2], dtype=torch.int32, device="cuda")
+    for cache in (small.cache, big):
+        fa.cache_append(cache, kn, vn, small.cu, small.lens)
+    a = fa.attention_forward_tree(q, small.cache, small.cu, small.lens, 3)
+    b = fa.attention_forward_tree(q, big, small.cu, small.lens, 3)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    check_attention(small, q, *a, 1 / d ** 0.5)
+    one[0, 1] = 2
+    for cache in (small.cache, big):
+        fa.cache_keep(cache, small.lens, one, two)
+    x, y = (fa.cache_read(cache, small.lens + 2, 152) for cache in (small.cache, big))
+    fa.fa_check_status()
+    assert torch.equal(x[0], y[0]) and torch.equal(x[1], y[1])
+
+
 @pytest.mark.parametrize("n", [1, 40])
 @pytest.mark.parametrize("fp8", [False, True])
 def test_long_peaked_rows(fp8, n):
