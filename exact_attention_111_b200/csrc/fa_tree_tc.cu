@@ -42,8 +42,6 @@ struct BigCfg {
   // exactly the launch's, so every increase is satisfied.
   static constexpr int kLaunchRegs = 128, kRegSoftmax = 176, kRegCorr = 88, kRegOther = 72;
   static_assert(2 * kRegSoftmax + kRegCorr + kRegOther <= 4 * kLaunchRegs, "register shares");
-  // exp2 pairs per 8 on the FMA pipe's polynomial (as in the dense forward)
-  static constexpr int kPolyOf8 = D == 64 ? 2 : 0;
 };
 
 // A segment: the CTA's run of tiles [kt0, kt0 + n) of one unit; nu of them can be seen by some row.
@@ -141,8 +139,9 @@ __device__ __forceinline__ uint32_t next_eref(uint32_t eref, uint32_t ev, bool f
 
 // Expand one tile (128 rows of D codes, as TMA staged them) into a ring tile: warp wi of nW.  A pass
 // of a warp is 32 / kLanes rows; row factors are computed once, two or one per lane, and
-// shuffled.  `read` is arrived on once the codes are in registers.  clean (V): rows from `keys` on become
-// zero and NaN codes too; returns whether there were.
+// shuffled.  clean (V): rows from `keys` on become zero and NaN codes too; returns whether there were.
+// `read` is arrived on once every code has been used.  (Arriving behind the last loads, before their values
+// are used, let the next copy overtake the loads: whole V tiles came out wrong.)
 template <int D, int nW>
 __device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, const uint8_t* scales, int e, int wi,
                                             uint64_t* read, bool clean, int keys) {
@@ -174,7 +173,6 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, 
       x[i][1] = *reinterpret_cast<const uint2*>(src + 8 - 8 * sw);
       fi[i] = __shfl_sync(0xffffffffu, kF > 1 && p * kW >= 32 ? f[kF - 1] : f[0], (p * kW) % 32 + sub);
     }
-    if (i0 + 2 == kPasses) mbar_arrive(read);
     if (clean) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
@@ -208,6 +206,7 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, 
       }
     }
   }
+  mbar_arrive(read);
   return odd;
 }
 
@@ -729,7 +728,9 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const float2 x = fma2(make_float2(s[32 * h + 2 * i], s[32 * h + 2 * i + 1]), sl2v, mnegv);
-            const float2 p = (((16 * h + i) & 7) < C::kPolyOf8) ? exp2_poly2(x) : make_float2(ex2(x.x), ex2(x.y));
+            // (a share on the FMA pipe's polynomial, as the dense forward has at d = 64, costs the LSE
+            // three digits, and at d = 128 4 to 6 % of time)
+            const float2 p = make_float2(ex2(x.x), ex2(x.y));
             acc[i & 3] = add2(acc[i & 3], p);
             pk[i] = pack2<kMmaFp16>(p.x, p.y);            // at most half a 16-bit step; the sum keeps 32 bits
           }

@@ -144,6 +144,36 @@ def test_values_of_the_prefix_beside_new_tokens(dtype, fp8, n, mask):
     assert not torch.isfinite(o[:, 2:, [5, 9, 40]]).any()
 
 
+@pytest.mark.parametrize("d,fp8,T,G", [(64, True, 250, 12), (128, True, 250, 12), (64, False, 250, 12), (64, True, 40, 5),
+                                       (64, True, 1, 4), (128, True, 1, 8)])
+def test_many_short_units_many_times(d, fp8, T, G):
+    """Units of a few tiles each, so that every role of the kernel runs ahead of the others and across
+    units; the results are the same bits every time, and right."""
+    counts = [max(1, T - 10 * b) for b in range(7)]
+    c = Case([79, 80, 161, 120, 125, 113, 129], counts, 5, d, 128, BF, fp8, seed=T + d)
+    c.put(c.new(5), c.new(5))
+    q = c.new(5 * G).cuda()
+    o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, T)
+    K, V = (torch.from_numpy(x).cuda() for x in c.values())
+    for b in range(c.B):                                 # fp64 on the GPU: the same definition, no bound per row
+        n, a, e = c.lens_l[b] + counts[b], c.cu_l[b], c.cu_l[b + 1]
+        pos = torch.arange(n)
+        pg, r = torch.from_numpy(c.table_np[b][pos // 128]).long().cuda(), (pos % 128).cuda()
+        k, v = (x[pg, :, r].transpose(0, 1) for x in (K, V))
+        x = torch.einsum("tgd,gnd->gtn", q[a:e].double().view(-1, 5, G, d).transpose(1, 2).reshape(-1, 5, d),
+                         k).div(d ** 0.5).view(5, e - a, G, n)
+        seen = torch.arange(n, device="cuda")[None, :] <= c.lens_l[b] + torch.arange(e - a, device="cuda")[:, None]
+        p = torch.softmax(x.masked_fill(~seen[None, :, None], float("-inf")), -1)
+        want = torch.einsum("gtkn,gnd->tgkd", p, v).reshape(e - a, 5 * G, d)
+        # P and O rounded to bf16: 2 * 2^-8 of sum p |v| <= max |v| over the visible keys
+        bound = 2.1 * 2.0 ** -8 * float(v.abs().max())
+        assert float((o[a:e].double() - want).abs().max()) <= bound
+    for _ in range(30):
+        o2, lse2 = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, T)
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    fa.fa_check_status()
+
+
 def test_rows_behind_four_gigabytes():
     """A cache whose K and V are over 4 GB each: positions in its last pages."""
     pages, Hk, page, d = 40000, 8, 64, 128
