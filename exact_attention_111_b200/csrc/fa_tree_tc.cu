@@ -140,11 +140,11 @@ __device__ __forceinline__ uint32_t next_eref(uint32_t eref, uint32_t ev, bool f
 // Expand one tile (128 rows of D codes, as TMA staged them) into a ring tile: warp wi of nW.  A pass
 // of a warp is 32 / kLanes rows; row factors are computed once, two or one per lane, and
 // shuffled.  clean (V): rows from `keys` on become zero and NaN codes too; returns whether there were.
-// `read` is arrived on once every code has been used.  (Arriving behind the last loads, before their values
-// are used, let the next copy overtake the loads: whole V tiles came out wrong.)
+// The caller releases the staging behind the stores and the proxy fence.  (Released behind the last loads,
+// before their values were used, the next copy got in first: whole V tiles came out wrong.)
 template <int D, int nW>
 __device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, const uint8_t* scales, int e, int wi,
-                                            uint64_t* read, bool clean, int keys) {
+                                            bool clean, int keys) {
   constexpr int kLanes = D / 16, kW = 32 / kLanes, kF = kTile / nW / 32, kPasses = kTile / (nW * kW);
   const int lane = lane_id();
   const int chunk = lane % kLanes, sub = lane / kLanes;
@@ -206,7 +206,6 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, 
       }
     }
   }
-  mbar_arrive(read);
   return odd;
 }
 
@@ -305,9 +304,10 @@ __device__ void expand_k_role(const TreeArgs& a, BigShared& sh, uint8_t* sK, con
         *reinterpret_cast<volatile float*>(&sh.vref[n & 7]) = scale_value(en);
       }
       eref = en;
-      expand_tile<D, 2>(sC, sK + s * (kTile * D * 2), sh.scales[0], (int)ek, wi, &sh.c_empty[0], false, 0);
+      expand_tile<D, 2>(sC, sK + s * (kTile * D * 2), sh.scales[0], (int)ek, wi, false, 0);
       fence_async_smem();
       mbar_arrive(&sh.k_full[s]);
+      mbar_arrive(&sh.c_empty[0]);
     }
   }
 }
@@ -556,11 +556,12 @@ __global__ void __launch_bounds__(512, 1)
         if (!__all_sync(0xffffffffu, go)) return false;
         const int keys = e.s.len + e.s.T - (e.kt0 + u) * kChunk;
         eref = next_eref(eref, top_scale(sh.scales[2], keys), u == 0);
-        if (expand_tile<D, 4>(sC + C::kCodes, sV + s * C::kTileBytes, sh.scales[2], (int)eref, wq, &sh.c_empty[1],
+        if (expand_tile<D, 4>(sC + C::kCodes, sV + s * C::kTileBytes, sh.scales[2], (int)eref, wq,
                               tail_tile(e, e.kt0 + u), keys))
           for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 1]) = seg[q] + 1;
         fence_async_smem();
         mbar_arrive(&sh.v_full[s]);
+        mbar_arrive(&sh.c_empty[1]);
         return true;
       };
       if constexpr (kFp8) {
