@@ -14,6 +14,12 @@
 // eight are merged through shared memory.  (With a ring of its own for each warp, filled by the warp, the
 // copies' issue took 700 of a step's 2000 cycles; a ninth warp filling the eight rings was the bottleneck.)
 //
+// Measured: a decoding step of 64 sequences of 1024 to 8191 keys, 32 query and 8 key heads of 128, bf16: 177
+// us, 6.3 TB/s of the cache's bytes (98 % of the copy rate, DRAM 77 % busy by its own count).  One token over
+// 131072 E4M3 keys, 32 query and 4 key heads of 128: 36 us against 21 of bytes; a step of 32 keys takes
+// some 2100 cycles of dependent loads, conversions, products and exponentials on two warps a scheduler,
+// and 4 us go into the start and the merges.  One token of 1023 keys, 16 heads of 64: 8.2 us, all latency.
+//
 // The products are made transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): keys and columns
 // fill the 16-wide side and rows come in eights, so four or eight query heads of a group cost
 // half of what a 16-row tile would, in products, exponentials and registers.

@@ -13,6 +13,16 @@
 // (16-bit) over the first 64 columns of its S.  Per tile u: O_q += P_q V(u-1), then S_q = Q_q K(u)^T, so
 // a finished S_q(u) also says that O_q holds every earlier product.
 //
+// Why two query tiles: K and V come from L2 or HBM once for 256 rows, and one tile's softmax runs beside the
+// other's products.  What bounds it: per 128 keys 2048 cycles of MMA and 2048 of exponentials (16 a clock);
+// a tile pair takes about 3100 cycles at 16 bits (softmax 1850, then 1200 until the next S: P V and S
+// behind the other tile's).  Issue matters: the MMA warp walks converged with its operands in uniform
+// registers (trees of 64 tokens 162 -> 156 us).  E4M3: about 5700 cycles; K's staging and expansion (3200 +
+// 2700 cycles, one buffer: shared memory is full at d = 128) set the pace.  Measured in bursts (at sustained
+// load the clock falls and the first takes 175 us): 8 trees of up to 64 tokens over up to 16384 keys, 64
+// query and 8 key heads of 128, bf16: 158 us, 695 TFLOP/s; 2 chunks of 512 over 16000 keys, 32 and 8 heads,
+// fp16: 137 us, 758 TFLOP/s; 16 trees of up to 48 over up to 8000 E4M3 keys: 148 us, 358 TFLOP/s.
+//
 // A masked product is 0 * v, which is not 0 where v is not finite.  Tiles that hold new tokens (which some
 // rows see and others do not) or reach past the end are therefore read once more by the correction
 // warps before their product: rows past the sequence's end become zero, and values that are not
