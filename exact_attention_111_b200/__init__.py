@@ -565,11 +565,11 @@ class KVCache:
         self.args = bytes(args)
         self._per_sequence, self._bounds = (self.B,), (self.B + 1,)
 
-    def _ints(self, **named):
-        """Check int32 tensors given as name=(tensor, shape)."""
-        for name, (t, shape) in named.items():
-            if not (t.dtype is _torch.int32 and t.shape == shape and t.is_contiguous() and t.get_device() == self.index):
-                raise ValueError(f"expected {name} as a contiguous int32 tensor {list(shape)} on the cache's device")
+    def _ints(self, name, t, shape):
+        """The address of an int32 tensor after its checks."""
+        if t.dtype is _torch.int32 and t.shape == shape and t.is_contiguous() and t.get_device() == self.index:
+            return t.data_ptr()
+        raise ValueError(f"expected {name} as a contiguous int32 tensor {list(shape)} on the cache's device")
 
     def _rows(self, name, t, heads):
         """(token, head) strides of a [total, heads, d] tensor."""
@@ -613,17 +613,16 @@ def cache_append(cache, k_new, v_new, cu_new, lens, stream=None):
     total = k_new.shape[0]
     if v_new.shape[0] != total or v_new.dtype is not k_new.dtype:
         raise ValueError("k_new and v_new differ in shape or type")
-    cache._ints(cu_new=(cu_new, cache._bounds), lens=(lens, cache._per_sequence))
     cache._call("fa_cache_append", _pack_append(
-        k_new.data_ptr(), v_new.data_ptr(), kt, kh, vt, vh, cu_new.data_ptr(), lens.data_ptr(), total,
-        cache._type(k_new), cache._raw_stream(stream)))
+        k_new.data_ptr(), v_new.data_ptr(), kt, kh, vt, vh, cache._ints("cu_new", cu_new, cache._bounds),
+        cache._ints("lens", lens, cache._per_sequence), total, cache._type(k_new), cache._raw_stream(stream)))
 
 
 def cache_read(cache, lens, N, dtype=None, k_out=None, v_out=None, stream=None):
     """The cache as dense (K, V), [B, Hk, N, d] 16-bit tensors with zeros past lens[b]
     (fa_cache_read).  ``dtype``: of an E4M3 cache's result, torch.bfloat16 (default) or float16;
     ``k_out``, ``v_out``: tensors to write to."""
-    cache._ints(lens=(lens, cache._per_sequence))
+    at = cache._ints("lens", lens, cache._per_sequence)
     shape = (cache.B, cache.Hk, N, cache.d)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else _torch.bfloat16 if cache.dtype == FA_E4M3 else cache.k.dtype
@@ -634,7 +633,7 @@ def cache_read(cache, lens, N, dtype=None, k_out=None, v_out=None, stream=None):
     for t in (k_out, v_out):
         if not (t.get_device() == cache.index and t.shape == shape and t.is_contiguous() and t.dtype is dtype):
             raise ValueError(f"expected k_out and v_out as contiguous {dtype} tensors {list(shape)}")
-    cache._call("fa_cache_read", _pack_read(lens.data_ptr(), k_out.data_ptr(), v_out.data_ptr(), N,
+    cache._call("fa_cache_read", _pack_read(at, k_out.data_ptr(), v_out.data_ptr(), N,
                                             cache._type(k_out), cache._raw_stream(stream)))
     return k_out, v_out
 
@@ -646,9 +645,9 @@ def cache_keep(cache, lens, kept, counts, stream=None):
     if kept.dim() != 2:
         raise ValueError("expected kept as [B, width]")
     width = kept.shape[1]
-    cache._ints(lens=(lens, cache._per_sequence), kept=(kept, (cache.B, width)), counts=(counts, cache._per_sequence))
-    cache._call("fa_cache_keep", _pack_keep(lens.data_ptr(), kept.data_ptr(), counts.data_ptr(), width,
-                                            cache._raw_stream(stream)))
+    cache._call("fa_cache_keep", _pack_keep(
+        cache._ints("lens", lens, cache._per_sequence), cache._ints("kept", kept, (cache.B, width)),
+        cache._ints("counts", counts, cache._per_sequence), width, cache._raw_stream(stream)))
 
 
 def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scale=None, workspace=None, o=None,
@@ -659,12 +658,12 @@ def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scal
     new tokens.  ``o``, ``lse``, ``workspace``: tensors to use instead of new ones.  Returns (O, LSE),
     [total, Hq, d] and fp32 [total, Hq]."""
     index = cache.index
-    if q.dim() != 3 or q.shape[1] < 1 or q.shape[1] % cache.Hk:
+    shape = q.shape
+    if len(shape) != 3 or shape[1] < 1 or shape[1] % cache.Hk:
         raise ValueError(f"expected q as [total, a multiple of {cache.Hk} heads, {cache.d}]")
-    total, Hq, d = q.shape
+    total, Hq, d = shape
     qt, qh = cache._rows("q", q, Hq)
     code = cache._type(q)
-    cache._ints(cu_new=(cu_new, cache._bounds), lens=(lens, cache._per_sequence))
     bits = words = 0
     if tree_mask is not None:
         if not (tree_mask.get_device() == index and tree_mask.dtype is _torch.int64 and tree_mask.dim() == 2
@@ -672,8 +671,8 @@ def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scal
             raise ValueError("expected tree_mask as a contiguous int64 tensor [total, words] on the cache's device")
         bits, words = tree_mask.data_ptr(), tree_mask.shape[1]
     if o is None:
-        o = _torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    elif o.shape != q.shape or o.dtype is not q.dtype:
+        o = _torch.empty(shape, dtype=q.dtype, device=q.device)
+    elif o.shape != shape or o.dtype is not q.dtype:
         raise ValueError("o and q differ in shape or type")
     ot, oh = cache._rows("o", o, Hq)
     if lse is None:
@@ -686,9 +685,9 @@ def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scal
     elif not (workspace.get_device() == index and workspace.is_contiguous()):
         raise ValueError("expected workspace as a contiguous tensor on the cache's device")
     cache._call("fa_fwd_tree", _pack_tree(
-        q.data_ptr(), o.data_ptr(), lse.data_ptr(), qt, qh, ot, oh, cu_new.data_ptr(), lens.data_ptr(), bits,
-        words, total, Hq, max_new, code, 1.0 / d ** 0.5 if scale is None else scale, workspace.data_ptr(),
-        workspace.nbytes, cache._raw_stream(stream)))
+        q.data_ptr(), o.data_ptr(), lse.data_ptr(), qt, qh, ot, oh, cache._ints("cu_new", cu_new, cache._bounds),
+        cache._ints("lens", lens, cache._per_sequence), bits, words, total, Hq, max_new, code,
+        1.0 / d ** 0.5 if scale is None else scale, workspace.data_ptr(), workspace.nbytes, cache._raw_stream(stream)))
     return o, lse
 
 
