@@ -18,7 +18,7 @@
 // us, 6.3 TB/s of the cache's bytes (98 % of the copy rate, DRAM 77 % busy by its own count).  One token over
 // 131072 E4M3 keys, 32 query and 4 key heads of 128: 36 us against 21 of bytes; a step of 32 keys takes
 // some 2100 cycles of dependent loads, conversions, products and exponentials on two warps a scheduler,
-// and 4 us go into the start and the merges.  One token of 1023 keys, 16 heads of 64: 8.2 us, all latency.
+// and 4 us go into the start and the merges.  One token of 1023 keys, 16 heads of 64: 7.7 us, all latency.
 //
 // The products are made transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): keys and columns
 // fill the 16-wide side and rows come in eights, so four or eight query heads of a group cost
@@ -650,8 +650,9 @@ __global__ void __launch_bounds__(384, 1)
 template <int D, bool kFp16>
 __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   constexpr int kV = D / 32;                              // columns per lane
+  constexpr int kBatch = 6;                               // parts of a warp whose loads are in flight together
   __shared__ float so[8][D];
-  __shared__ float sl[8];
+  __shared__ float sm[8], sl[8];
   grid_begin();
   const int c = blockIdx.x, lane = lane_id(), warp = warp_id();
   const int4 me = a.meta[2 * c];                          // last CTA, rows, first token, key head
@@ -659,39 +660,67 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeArgs a) {
   const int r = blockIdx.y;
   if (me.x < 0 || r >= me.y) return;
   const int n = me.x - c + 1;                             // parts: this CTA's and those of c + 1 .. me.x
-  auto at = [&](int i) { return (2LL * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r; };
-  float m = -INFINITY;
-  for (int i = lane; i < n; i += 32) m = fmaxf(m, a.part_ml[at(i) * 2]);
+  // Each warp sums its parts against its own maximum, so that their sums, maxima and values are loaded
+  // at once: what counts here is the number of loads that wait for one another.
+  float m = -INFINITY, l = 0.f, acc[kV] = {};
+  for (int i0 = warp; i0 < n; i0 += 8 * kBatch) {
+    float2 ml[kBatch];
+    float x[kBatch][kV];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float neg = m == -INFINITY ? 0.f : -m;
-  float l = 0.f, acc[kV] = {};
-#pragma unroll 4
-  for (int i = warp; i < n; i += 8) {
-    const long long k = at(i);
-    const float2 ml = *reinterpret_cast<const float2*>(a.part_ml + k * 2);
-    const float w = ex2(ml.x + neg);
-    l += w * ml.y;
+    for (int j = 0; j < kBatch; ++j) {
+      const int i = i0 + 8 * j;
+      ml[j] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-    for (int j = 0; j < kV; j += 2) {
-      const float2 x = *reinterpret_cast<const float2*>(a.part_o + k * D + lane * kV + j);
-      acc[j] += w * x.x;
-      acc[j + 1] += w * x.y;
+      for (int k = 0; k < kV; ++k) x[j][k] = 0.f;
+      if (i < n) {
+        const long long at = (2LL * (c + i) + (i == 0 ? 1 : 0)) * a.slot_rows + r;
+        ml[j] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+#pragma unroll
+        for (int k = 0; k < kV; k += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(a.part_o + at * D + lane * kV + k);
+          x[j][k] = v.x;
+          x[j][k + 1] = v.y;
+        }
+      }
+    }
+    float mn = m;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, ml[j].x);
+    const float neg = mn == -INFINITY ? 0.f : -mn;
+    const float f = ex2(m + neg);
+    m = mn;
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) acc[k] *= f;
+#pragma unroll
+    for (int j = 0; j < kBatch; ++j) {
+      const float w = ex2(ml[j].x + neg);
+      l += w * ml[j].y;
+#pragma unroll
+      for (int k = 0; k < kV; ++k) acc[k] += w * x[j][k];
     }
   }
 #pragma unroll
   for (int j = 0; j < kV; ++j) so[warp][lane * kV + j] = acc[j];
-  if (lane == 0) sl[warp] = l;
+  if (lane == 0) {
+    sm[warp] = m;
+    sl[warp] = l;
+  }
   __syncthreads();
   if (warp != 0) return;
+  m = -INFINITY;
+#pragma unroll
+  for (int w = 0; w < 8; ++w) m = fmaxf(m, sm[w]);
+  const float neg = m == -INFINITY ? 0.f : -m;
   l = 0.f;
 #pragma unroll
   for (int j = 0; j < kV; ++j) acc[j] = 0.f;
 #pragma unroll
   for (int w = 0; w < 8; ++w) {
-    l += sl[w];
+    const float f = ex2(sm[w] + neg);
+    l += f * sl[w];
 #pragma unroll
-    for (int j = 0; j < kV; ++j) acc[j] += so[w][lane * kV + j];
+    for (int j = 0; j < kV; ++j) acc[j] += f * so[w][lane * kV + j];
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
