@@ -16,7 +16,7 @@
 //
 // Measured: a decoding step of 64 sequences of 1024 to 8191 keys, 32 query and 8 key heads of 128, bf16: 177
 // us, 6.3 TB/s of the cache's bytes (98 % of the copy rate, DRAM 77 % busy by its own count).  One token over
-// 131072 E4M3 keys, 32 query and 4 key heads of 128: 36 us against 21 of bytes; a step of 32 keys takes
+// 131072 E4M3 keys, 32 query and 4 key heads of 128: 35 us against 21 of bytes; a step of 32 keys takes
 // some 2100 cycles of dependent loads, conversions, products and exponentials on two warps a scheduler,
 // and 4 us go into the start and the merges.  One token of 1023 keys, 16 heads of 64: 7.7 us, all latency.
 //

@@ -19,9 +19,9 @@
 // behind the other tile's).  Issue matters: the MMA warp walks converged with its operands in uniform
 // registers (trees of 64 tokens 162 -> 156 us).  E4M3: about 5700 cycles; K's staging and expansion (3200 +
 // 2700 cycles, one buffer: shared memory is full at d = 128) set the pace.  Measured in bursts (at sustained
-// load the clock falls and the first takes 175 us): 8 trees of up to 64 tokens over up to 16384 keys, 64
+// load the clock falls and the first takes 184 us): 8 trees of up to 64 tokens over up to 16384 keys, 64
 // query and 8 key heads of 128, bf16: 158 us, 695 TFLOP/s; 2 chunks of 512 over 16000 keys, 32 and 8 heads,
-// fp16: 137 us, 758 TFLOP/s; 16 trees of up to 48 over up to 8000 E4M3 keys: 148 us, 358 TFLOP/s.
+// fp16: 137 us, 758 TFLOP/s; 16 trees of up to 48 over up to 8000 E4M3 keys: 151 us, 352 TFLOP/s.
 //
 // A masked product is 0 * v, which is not 0 where v is not finite.  Tiles that hold new tokens (which some
 // rows see and others do not) or reach past the end are therefore read once more by the correction
