@@ -614,6 +614,7 @@ __global__ void __launch_bounds__(512, 1)
           if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
           const float al = sh.alpha[q][r];
           if (u > 0 && __any_sync(0xffffffffu, al != 1.f)) {
+            __syncwarp();
             tc_fence_after();
             const uint32_t tO = tmem + C::kOCol + q * D + lane_off;
 #pragma unroll 2
@@ -693,6 +694,7 @@ __global__ void __launch_bounds__(512, 1)
         const int kt = e.kt0 + u;
         ok = mbar_wait(&sh.s_full[q], cs & 1, abort_flag, st);
         if (__any_sync(0xffffffffu, !ok)) { ok = false; break; }
+        __syncwarp();                                     // as at P's stores
         tc_fence_after();
         uint32_t sr[128];
         tmem_ld32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
@@ -733,6 +735,7 @@ __global__ void __launch_bounds__(512, 1)
         const float mneg = (m == -INFINITY) ? 0.f : -m;
         const float2 sl2v = make_float2(sl2, sl2), mnegv = make_float2(mneg, mneg);
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        __syncwarp();                                     // P's stores are the whole warp's: rows may have parted above
 #pragma unroll
         for (int h = 0; h < 4; ++h) {
           uint32_t pk[16];
@@ -785,52 +788,54 @@ __global__ void __launch_bounds__(512, 1)
       for (int cc = 0; cc < D; cc += 32) {
         uint32_t o[32];
         if (e.nu > 0) {
+          __syncwarp();                                   // the load is the whole warp's; rows part below
           tmem_ld32_sync(tO + cc, o);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
-        if (!live) continue;
-        if (odd) {                                        // rare: see the top of the file
-          // keys of the segment's tiles that were made safe; j < 0 is the prefix
-          const int j1 = min(e.s.T, (e.kt0 + e.nu) * kChunk - e.s.len);
-          for (int j = max(e.kt0, e.s.len / kChunk) * kChunk - e.s.len; j < j1; ++j) {
-            if (!(visible32(a, e.s, t, j) & 1u)) continue;
-            const long long row = slot_row(a.c, e.b, e.h, (long long)e.s.len + j);
-            if (row < 0) continue;
+        if (live) {
+          if (odd) {                                      // rare: see the top of the file
+            // keys of the segment's tiles that were made safe; j < 0 is the prefix
+            const int j1 = min(e.s.T, (e.kt0 + e.nu) * kChunk - e.s.len);
+            for (int j = max(e.kt0, e.s.len / kChunk) * kChunk - e.s.len; j < j1; ++j) {
+              if (!(visible32(a, e.s, t, j) & 1u)) continue;
+              const long long row = slot_row(a.c, e.b, e.h, (long long)e.s.len + j);
+              if (row < 0) continue;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              if constexpr (kFp8) {
-                if ((a.c.v[row * D + cc + i] & 0x7F) == 0x7F) o[i] = 0x7FFFFFFFu;
-              } else {
-                constexpr uint32_t ex = kFp16 ? 0x7C00u : 0x7F80u;
-                const uint32_t x = reinterpret_cast<const uint16_t*>(a.c.v)[row * D + cc + i];
-                if ((x & ex) == ex) o[i] = __float_as_uint(__uint_as_float(o[i]) + unpack2<kFp16>(x).x);
+              for (int i = 0; i < 32; ++i) {
+                if constexpr (kFp8) {
+                  if ((a.c.v[row * D + cc + i] & 0x7F) == 0x7F) o[i] = 0x7FFFFFFFu;
+                } else {
+                  constexpr uint32_t ex = kFp16 ? 0x7C00u : 0x7F80u;
+                  const uint32_t x = reinterpret_cast<const uint16_t*>(a.c.v)[row * D + cc + i];
+                  if ((x & ex) == ex) o[i] = __float_as_uint(__uint_as_float(o[i]) + unpack2<kFp16>(x).x);
+                }
               }
             }
           }
-        }
-        if (whole) {
-          uint4* dst = reinterpret_cast<uint4*>(a.o + tk * a.o_tok + hq * a.o_head + cc);
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(a.o + tk * a.o_tok + hq * a.o_head + cc);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint4 w;
-            w.x = pack2<kFp16>(__uint_as_float(o[8 * i + 0]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
-            w.y = pack2<kFp16>(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
-            w.z = pack2<kFp16>(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
-            w.w = pack2<kFp16>(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
-            dst[i] = w;
-          }
-        } else {
-          // four columns of all rows, then the next four: a warp's stores are contiguous
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o) + ((long long)slot * (D / 4) + cc / 4) * a.slot_rows + r;
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            if constexpr (kFp8) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) o[4 * i + k] = __float_as_uint(__uint_as_float(o[4 * i + k]) * inv);
+            for (int i = 0; i < 4; ++i) {
+              uint4 w;
+              w.x = pack2<kFp16>(__uint_as_float(o[8 * i + 0]) * inv, __uint_as_float(o[8 * i + 1]) * inv);
+              w.y = pack2<kFp16>(__uint_as_float(o[8 * i + 2]) * inv, __uint_as_float(o[8 * i + 3]) * inv);
+              w.z = pack2<kFp16>(__uint_as_float(o[8 * i + 4]) * inv, __uint_as_float(o[8 * i + 5]) * inv);
+              w.w = pack2<kFp16>(__uint_as_float(o[8 * i + 6]) * inv, __uint_as_float(o[8 * i + 7]) * inv);
+              dst[i] = w;
             }
-            dst[(long long)i * a.slot_rows] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          } else {
+            // four columns of all rows, then the next four: a warp's stores are contiguous
+            uint4* dst = reinterpret_cast<uint4*>(a.part_o) + ((long long)slot * (D / 4) + cc / 4) * a.slot_rows + r;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if constexpr (kFp8) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) o[4 * i + k] = __float_as_uint(__uint_as_float(o[4 * i + k]) * inv);
+              }
+              dst[(long long)i * a.slot_rows] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            }
           }
         }
       }

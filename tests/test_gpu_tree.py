@@ -370,3 +370,20 @@ def test_lengths_that_cannot_be_are_reported():
     o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, 2)
     fa.fa_check_status()
     check_attention(c, q, o, lse, 1 / 8)
+
+
+@pytest.mark.parametrize("d,dtype,fp8", [(64, HF, False), (128, BF, False), (64, BF, True), (128, HF, True)])
+def test_units_that_end_anywhere_in_a_warp(d, dtype, fp8):
+    """Many-row units whose last warp has from one to all 32 of its rows, in whole units and in units cut
+    between CTAs, with values that are not finite: what the whole warp loads and what its rows do apart."""
+    for T in (33, 34, 47, 63, 64, 65, 95, 127, 129, 130, 159, 193, 255):
+        c = Case([3, 700], [T, T - 1], 1, d, 16, dtype, fp8, seed=T + d)
+        k, v = c.new(1), c.new(1)
+        for t, x in ((1, float("nan")), (T // 2, float("inf")), (T + 5, -float("inf"))):
+            v[t, :, t % 7::9] = x
+        c.put(k, v)
+        q = c.new(1).cuda()
+        bits = _masks("random", c, seed=T)
+        o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, T, tree_mask=bits)
+        fa.fa_check_status()
+        check_attention(c, q, o, lse, 1 / d ** 0.5, bits, f"T={T}", nan_ok=True)
