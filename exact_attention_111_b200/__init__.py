@@ -20,11 +20,16 @@ ones, ``cache_read`` reads it back as dense tensors:
     o, lse = attention_forward_tree(q, cache, cu, lens, max_new, tree_mask=tree_mask(parents, cu))
     cache_keep(cache, lens, kept, counts);  lens += counts
 
+``stream``: the stream (or its handle) a call's kernels run on, torch's current one by default.  What a
+call allocates belongs to that stream; what the caller passes has to be ready on it, and to live until it is
+done.
+
 There is no fallback: if ``libfa.so`` is missing or a call fails, an exception is raised.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import struct
@@ -212,6 +217,19 @@ def _stream(stream):
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _made_on(stream, device):
+    """Context for the tensors that a call on `stream` makes for itself: torch's allocator keeps a block
+    for the stream that was current when it was made, and gives it to that stream alone.  Made
+    under another stream than the kernels', a result could lie where earlier work is not done, and a
+    scratch block would be given away while the kernels still use it."""
+    import torch
+    if stream is None:
+        return contextlib.nullcontext()
+    if isinstance(stream, int):                          # (an external stream of handle 0 would be a new stream)
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    return torch.cuda.stream(stream)
 
 
 def _check(rc: int, what: str):
@@ -419,8 +437,9 @@ def attention_forward(q, k, v, causal=False, blockmask=None, scale=None, o_fp32=
     _check_qkv(q, k, v)
     B, H, N, d = q.shape
     scale = (1.0 / d ** 0.5) if scale is None else scale
-    o = torch.empty(q.shape, dtype=torch.float32 if o_fp32 else q.dtype, device=q.device)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    with _made_on(stream, q.device):
+        o = torch.empty(q.shape, dtype=torch.float32 if o_fp32 else q.dtype, device=q.device)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     fa_fwd_ex(q, k, v, o, lse, B, H, N, d, scale, causal, blockmask, _dtype_code(q), o_fp32,
               visit_log, stream, dropout_p=dropout_p, dropout_seed=dropout_seed)
     return o, lse
@@ -437,11 +456,12 @@ def attention_forward_splitkv(q, k, v, causal=False, blockmask=None, scale=None,
     if num_splits is None:
         sms = torch.cuda.get_device_properties(q.device).multi_processor_count
         num_splits = fa_splitkv_choose(B, H, N, causal, sms)
-    o = torch.empty_like(q)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     nbytes = fa_fwd_splitkv_workspace_bytes(B, H, N, d, num_splits)
-    if workspace is None and num_splits > 1:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+    with _made_on(stream, q.device):
+        o = torch.empty_like(q)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+        if workspace is None and num_splits > 1:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     fa_fwd_splitkv(q, k, v, o, lse, B, H, N, d, scale, causal, blockmask, num_splits, workspace,
                    0 if workspace is None else workspace.numel(), stream)
     return o, lse, num_splits
@@ -456,8 +476,9 @@ def attention_forward_partial(q, k, v, key_offset=0, causal=False, blockmask=Non
     B, H, N, d = q.shape
     Nk = k.shape[2]
     scale = (1.0 / d ** 0.5) if scale is None else scale
-    o = torch.empty((B, H, N, d), dtype=torch.float32, device=q.device)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
+    with _made_on(stream, q.device):
+        o = torch.empty((B, H, N, d), dtype=torch.float32, device=q.device)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q.device)
     fa_fwd_partial(q, k, v, o, lse, B, H, N, Nk, d, key_offset, scale, causal, blockmask,
                    _dtype_code(q), stream)
     return o, lse
@@ -473,8 +494,9 @@ def lse_merge(o_parts, lse_parts, out_dtype=None, stream=None):
     for t in list(o_parts) + list(lse_parts):
         if not (t.is_cuda and t.is_contiguous() and t.dtype == torch.float32):
             raise ValueError("parts must be contiguous fp32 CUDA tensors")
-    o = torch.empty((B, H, N, d), dtype=out_dtype, device=o_parts[0].device)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=o_parts[0].device)
+    with _made_on(stream, o_parts[0].device):
+        o = torch.empty((B, H, N, d), dtype=out_dtype, device=o_parts[0].device)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=o_parts[0].device)
     fa_lse_merge(list(o_parts), list(lse_parts), o, lse, B, H, N, d, code, stream)
     return o, lse
 
@@ -489,10 +511,11 @@ def attention_forward_fp8(q8, k8, v8, descale_q, descale_k, descale_v, causal=Fa
             raise ValueError("expected contiguous 8-bit CUDA tensors of shape [B, H, N, 128]")
     B, H, N, d = q8.shape
     scale = (1.0 / d ** 0.5) if scale is None else scale
-    o = torch.empty((B, H, N, d), dtype=torch.float32 if o_fp32 else torch.bfloat16, device=q8.device)
-    lse = torch.empty((B, H, N), dtype=torch.float32, device=q8.device)
-    if workspace is None:
-        workspace = torch.empty(max(fa_fwd_fp8_workspace_bytes(B, H, N, d), 1), dtype=torch.uint8, device=q8.device)
+    with _made_on(stream, q8.device):
+        o = torch.empty((B, H, N, d), dtype=torch.float32 if o_fp32 else torch.bfloat16, device=q8.device)
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=q8.device)
+        if workspace is None:
+            workspace = torch.empty(max(fa_fwd_fp8_workspace_bytes(B, H, N, d), 1), dtype=torch.uint8, device=q8.device)
     fa_fwd_fp8(q8, k8, v8, descale_q, descale_k, descale_v, o, lse, B, H, N, d, scale, causal, blockmask, o_fp32,
                workspace, workspace.numel(), stream)
     return o, lse
@@ -510,11 +533,12 @@ def attention_backward(q, k, v, o, lse, dout, causal=False, blockmask=None, scal
     scale = (1.0 / d ** 0.5) if scale is None else scale
     nbytes = (fa_bwd_workspace_bytes_split(B, H, N, d, query_splits) if query_splits > 1
               else fa_bwd_workspace_bytes_ex(B, H, N, d, deterministic))
-    if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
-    dq = torch.empty_like(q)
-    dk = torch.empty_like(k)
-    dv = torch.empty_like(v)
+    with _made_on(stream, q.device):
+        if workspace is None:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        dq = torch.empty_like(q)
+        dk = torch.empty_like(k)
+        dv = torch.empty_like(v)
     fa_bwd_ex(q, k, v, o, lse, dout, dq, dk, dv, B, H, N, d, scale, causal, blockmask,
               _dtype_code(q), visit_log, workspace, workspace.numel(), stream, deterministic=deterministic,
               dropout_p=dropout_p, dropout_seed=dropout_seed, query_splits=query_splits)
@@ -626,10 +650,11 @@ def cache_read(cache, lens, N, dtype=None, k_out=None, v_out=None, stream=None):
     shape = (cache.B, cache.Hk, N, cache.d)
     if dtype is None:
         dtype = k_out.dtype if k_out is not None else _torch.bfloat16 if cache.dtype == FA_E4M3 else cache.k.dtype
-    if k_out is None:
-        k_out = _torch.empty(shape, dtype=dtype, device=cache.device)
-    if v_out is None:
-        v_out = _torch.empty(shape, dtype=dtype, device=cache.device)
+    with _made_on(stream, cache.device):
+        if k_out is None:
+            k_out = _torch.empty(shape, dtype=dtype, device=cache.device)
+        if v_out is None:
+            v_out = _torch.empty(shape, dtype=dtype, device=cache.device)
     for t in (k_out, v_out):
         if not (t.get_device() == cache.index and t.shape == shape and t.is_contiguous() and t.dtype is dtype):
             raise ValueError(f"expected k_out and v_out as contiguous {dtype} tensors {list(shape)}")
@@ -655,8 +680,8 @@ def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scal
     """Attention of new tokens q [total, Hq, d] over the cache that already holds their rows
     (fa_fwd_tree).  ``tree_mask``: None for a chain (token t sees new tokens j <= t), or int64
     [total, words] visibility bits (see ``tree_mask``).  ``max_new``: at least every sequence's number of
-    new tokens.  ``o``, ``lse``, ``workspace``: tensors to use instead of new ones.  Returns (O, LSE),
-    [total, Hq, d] and fp32 [total, Hq]."""
+    new tokens.  ``o``, ``lse``, ``workspace``: tensors to use instead of new ones, which belong to
+    ``stream``.  Returns (O, LSE), [total, Hq, d] and fp32 [total, Hq]."""
     index = cache.index
     shape = q.shape
     if len(shape) != 3 or shape[1] < 1 or shape[1] % cache.Hk:
@@ -670,19 +695,22 @@ def attention_forward_tree(q, cache, cu_new, lens, max_new, tree_mask=None, scal
                 and tree_mask.is_contiguous() and tree_mask.shape[0] == total):
             raise ValueError("expected tree_mask as a contiguous int64 tensor [total, words] on the cache's device")
         bits, words = tree_mask.data_ptr(), tree_mask.shape[1]
-    if o is None:
-        o = _torch.empty(shape, dtype=q.dtype, device=q.device)
-    elif o.shape != shape or o.dtype is not q.dtype:
+    if o is None or lse is None or workspace is None:
+        with _made_on(stream, cache.device):
+            if o is None:
+                o = _torch.empty(shape, dtype=q.dtype, device=cache.device)
+            if lse is None:
+                lse = _torch.empty((total, Hq), dtype=_torch.float32, device=cache.device)
+            if workspace is None:
+                workspace = _torch.empty(fa_fwd_tree_workspace_bytes(total, Hq, cache.Hk, d), dtype=_torch.uint8,
+                                         device=cache.device)
+    if o.shape != shape or o.dtype is not q.dtype:
         raise ValueError("o and q differ in shape or type")
     ot, oh = cache._rows("o", o, Hq)
-    if lse is None:
-        lse = _torch.empty((total, Hq), dtype=_torch.float32, device=q.device)
-    elif not (lse.get_device() == index and lse.dtype is _torch.float32 and lse.shape == (total, Hq)
-              and lse.is_contiguous()):
+    if not (lse.get_device() == index and lse.dtype is _torch.float32 and lse.shape == (total, Hq)
+            and lse.is_contiguous()):
         raise ValueError("expected lse as a contiguous float32 tensor [total, Hq]")
-    if workspace is None:
-        workspace = _torch.empty(fa_fwd_tree_workspace_bytes(total, Hq, cache.Hk, d), dtype=_torch.uint8, device=q.device)
-    elif not (workspace.get_device() == index and workspace.is_contiguous()):
+    if not (workspace.get_device() == index and workspace.is_contiguous()):
         raise ValueError("expected workspace as a contiguous tensor on the cache's device")
     cache._call("fa_fwd_tree", _pack_tree(
         q.data_ptr(), o.data_ptr(), lse.data_ptr(), qt, qh, ot, oh, cache._ints("cu_new", cu_new, cache._bounds),
