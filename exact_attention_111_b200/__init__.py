@@ -551,7 +551,25 @@ class KVCache:
     ``k``, ``v``: [pages, Hk, page_size, d] CUDA tensors, contiguous, bf16 or fp16, or E4M3 codes
     (torch.float8_e4m3fn or uint8) with ``k_scale``, ``v_scale`` [pages, Hk, page_size] E8M0 codes
     (torch.float8_e8m0fnu or uint8).  ``page_table``: int32 [B, max_pages]; its contents may change
-    between calls.  The object keeps the tensors alive and allocates nothing."""
+    between calls.  The object keeps the tensors alive and allocates nothing.  These
+    attributes cannot be set: the calls use the addresses and sizes taken here, so another table or other
+    pages need another KVCache."""
+
+    _fixed = frozenset(("k", "v", "k_scale", "v_scale", "page_table", "device", "index", "dtype", "pages", "Hk",
+                        "page_size", "d", "B", "max_pages", "args", "_per_sequence", "_bounds"))
+
+    def __setattr__(self, name, value):
+        if name in self._fixed:
+            raise AttributeError(f"a KVCache's {name} cannot be set: make another KVCache")
+        object.__setattr__(self, name, value)
+
+    def __delattr__(self, name):
+        if name in self._fixed:
+            raise AttributeError(f"a KVCache's {name} cannot be deleted")
+        object.__delattr__(self, name)
+
+    def __reduce__(self):                                # a copy has the addresses of its own tensors
+        return KVCache, (self.k, self.v, self.page_table, self.k_scale, self.v_scale)
 
     def __init__(self, k, v, page_table, k_scale=None, v_scale=None):
         global _torch
@@ -567,27 +585,25 @@ class KVCache:
                 if t is None or not (t.is_cuda and t.is_contiguous() and t.element_size() == 1
                                      and t.shape == k.shape[:3]):
                     raise ValueError("an E4M3 cache needs k_scale and v_scale, [pages, Hk, page_size] E8M0 codes")
-            self.dtype = FA_E4M3
+            dtype = FA_E4M3
         else:
             if k_scale is not None or v_scale is not None:
                 raise ValueError("scales belong to an E4M3 cache")
-            self.dtype = _dtype_code(k)
+            dtype = _dtype_code(k)
         if not (page_table.is_cuda and page_table.dtype == torch.int32 and page_table.dim() == 2
                 and (page_table.shape[1] == 1 or page_table.stride(1) == 1)):
             raise ValueError("expected page_table as an int32 CUDA tensor [B, max_pages]")
-        self.k, self.v, self.k_scale, self.v_scale, self.page_table = k, v, k_scale, v_scale, page_table
-        self.device = k.device
-        self.index = k.get_device()
         for t in (v, k_scale, v_scale, page_table):
             if t is not None and t.device != k.device:
                 raise ValueError("the cache's tensors are on different devices")
-        self.pages, self.Hk, self.page_size, self.d = k.shape
-        self.B, self.max_pages = page_table.shape
-        args = CacheArgs(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), self.pages, self.Hk,
-                         self.page_size, self.d, self.dtype, self.B, self.max_pages,
-                         page_table.stride(0) if self.B > 1 else max(self.max_pages, 1))
-        self.args = bytes(args)
-        self._per_sequence, self._bounds = (self.B,), (self.B + 1,)
+        pages, Hk, page_size, d = k.shape
+        B, max_pages = page_table.shape
+        args = CacheArgs(_ptr(k), _ptr(v), _ptr(k_scale), _ptr(v_scale), _ptr(page_table), pages, Hk, page_size, d, dtype,
+                         B, max_pages, page_table.stride(0) if B > 1 else max(max_pages, 1))
+        self.__dict__.update(
+            k=k, v=v, k_scale=k_scale, v_scale=v_scale, page_table=page_table, device=k.device, index=k.get_device(),
+            dtype=dtype, pages=pages, Hk=Hk, page_size=page_size, d=d, B=B, max_pages=max_pages, args=bytes(args),
+            _per_sequence=(B,), _bounds=(B + 1,))
 
     def _ints(self, name, t, shape):
         """The address of an int32 tensor after its checks."""

@@ -3,6 +3,8 @@ fp64 oracle.  Quantising has one right answer for every code, so the comparison 
 
 from __future__ import annotations
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -174,3 +176,30 @@ def test_bad_pages_and_lists_are_reported_and_touch_nothing():
     _range_error()
     for n in before:
         assert torch.equal(before[n], c.gpu[n]), n
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_the_tensors_of_a_cache_are_fixed(fp8):
+    """The calls use the addresses that the KVCache took, so no other tensor can be put in one's place, and a
+    copy has its own."""
+    c = Case([20, 3], [2, 1], 2, 64, 16, BF, fp8, seed=3)
+    for name in ("k", "v", "k_scale", "v_scale", "page_table", "pages", "B", "args"):
+        with pytest.raises(AttributeError):
+            setattr(c.cache, name, None)
+        with pytest.raises(AttributeError):
+            delattr(c.cache, name)
+    c.cache.layer = 3                                    # the caller's own
+    wide = torch.cat([c.table, c.table[:, :1]], 1).contiguous()
+    bigger = fa.KVCache(c.cache.k, c.cache.v, wide, c.cache.k_scale, c.cache.v_scale)
+    assert bigger.max_pages == c.cache.max_pages + 1
+    other = copy.deepcopy(c.cache)
+    assert other.k.data_ptr() != c.cache.k.data_ptr() and other.args != c.cache.args
+    before = {n: _bits(x) for n, x in c.gpu.items()}
+    k, v = c.new(2).cuda(), c.new(2).cuda()
+    fa.cache_append(other, k, v, c.cu, c.lens)           # the copy's rows, not the first cache's
+    for n in before:
+        assert np.array_equal(before[n], _bits(c.gpu[n])), n
+    fa.cache_append(c.cache, k, v, c.cu, c.lens)
+    fa.fa_check_status()
+    for n in before:
+        assert np.array_equal(_bits(getattr(other, n)), _bits(c.gpu[n])), n
