@@ -100,10 +100,17 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
       xv[i] = *reinterpret_cast<const uint4*>(a.v + tok * a.v_tok + h * a.v_head + col);
     }
   }
+  if (w == 0) {                                     // one warp looks the whole list of bounds over
+    bool bad = a.cu[0] < 0 || a.cu[a.c.B] > a.total;
+    for (int i = lane; i < a.c.B; i += 32) bad |= a.cu[i] > a.cu[i + 1];
+    if (bad) flag_range(a.c);
+  }
   const int b = owner_of(a.cu, a.c.B, tok);
   if (b < 0) return;                                // past the last sequence: not a token
-  const int len = a.lens[b];
-  const long long row = len < 0 ? -1 : slot_row(a.c, b, 0, (long long)len + (tok - a.cu[b]));
+  const int len = a.lens[b], c0 = a.cu[b], c1 = a.cu[b + 1];
+  // (a list that decreases may have led anywhere)
+  const bool bounds = c0 >= 0 && c0 <= tok && tok < c1 && c1 <= a.total;
+  const long long row = len < 0 || !bounds ? -1 : slot_row(a.c, b, 0, (long long)len + (tok - c0));
   if (row < 0) {
     flag_range(a.c);
     return;                                         // the whole warp: one token

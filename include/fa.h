@@ -424,7 +424,9 @@ typedef struct {
  *   k_new, v_new : in, [total, Hk, d] (dtype), the d values contiguous, strides in elements and
  *                  multiples of 8, 16-byte aligned (slices of a fused projection will do)
  *   cu_new       : device int32 [B + 1], non-decreasing; tokens outside cu_new[0] ..
- *                  cu_new[B] - 1 are ignored (a padded batch)
+ *                  cu_new[B] - 1 are ignored (a padded batch).  A list that decreases or leaves
+ *                  0 .. total is reported as FA_ERR_RANGE, and a sequence whose bounds do is not
+ *                  written.  (total 0 launches nothing, so it checks nothing.)
  *   lens         : device int32 [B], positions held before the call (not changed)
  * One launch.
  */

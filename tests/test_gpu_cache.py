@@ -203,3 +203,37 @@ def test_the_tensors_of_a_cache_are_fixed(fp8):
     fa.fa_check_status()
     for n in before:
         assert np.array_equal(_bits(getattr(other, n)), _bits(c.gpu[n])), n
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_append_reports_bounds_that_cannot_be(fp8):
+    """New-token bounds outside 0 .. total, and lists that decrease: reported, and no row goes to a slot that is
+    not its own."""
+    c = Case([20, 20, 7], [2, 2, 0], 2, 64, 16, BF, fp8, seed=3)
+    k, v = c.new(2), c.new(2)
+    gk, gv = k.cuda(), v.cuda()
+    want = _expect_append(c, k, v)
+    before = {n: _bits(x) for n, x in c.gpu.items()}
+    wrong = [[-1, 2, 4, 4], [-1, 1, 3, 4], [0, 2, 5, 5], [0, 3, 2, 4], [2, 0, 4, 4], [0, 2, 4, 3], [0, 2, 4, 2 ** 31 - 1],
+             [-2 ** 31, 2, 4, 4]]
+    for cu in wrong:
+        for n, x in c.gpu.items():
+            x.copy_(torch.from_numpy(before[n]).view(x.dtype).view(x.shape))
+        fa.cache_append(c.cache, gk, gv, torch.tensor(cu, dtype=torch.int32).cuda(), c.lens)
+        _range_error()
+        for b in range(3):
+            for pos in range(c.lens_l[b]):               # what a sequence holds stays
+                p, r = ora.slot(c.table_np, b, pos, c.page)
+                for n, x in c.gpu.items():
+                    was = torch.from_numpy(before[n]).view(x.dtype).view(x.shape)
+                    assert np.array_equal(_bits(x[p, :, r]), _bits(was[p, :, r])), (cu, b, pos, n)
+    for n, x in c.gpu.items():
+        x.copy_(torch.from_numpy(before[n]).view(x.dtype).view(x.shape))
+    fa.cache_append(c.cache, gk, gv, c.cu, c.lens)
+    fa.fa_check_status()
+    for n in want:
+        assert np.array_equal(_bits(c.gpu[n]), _bits(want[n])), n
+    # a padded batch: tokens in front of the first sequence and behind the last are ignored
+    some = torch.tensor([1, 2, 3, 3], dtype=torch.int32).cuda()
+    fa.cache_append(c.cache, gk, gv, some, c.lens)
+    fa.fa_check_status()
