@@ -846,7 +846,8 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   if (!x.cu_new || !x.lens || !aligned(x.cu_new, 4) || !aligned(x.lens, 4)) return FA_ERR_INVALID_ARG;
   if (x.tree_mask != nullptr && (x.mask_words < 1 || (long long)x.mask_words * 64 < x.max_new)) return FA_ERR_INVALID_ARG;
   if (!aligned(x.tree_mask, 8)) return FA_ERR_INVALID_ARG;
-  if (x.total == 0 || x.max_new == 0) return FA_OK;
+  // max_new 0 says that there are no new tokens.  With a workspace the kernel looks whether that is so.
+  if (x.total == 0 || (x.max_new == 0 && x.workspace == nullptr)) return FA_OK;
   if (!x.q || !x.o || !x.lse || !aligned(x.q, 16) || !aligned(x.o, 16) || !aligned(x.lse, 4)) return FA_ERR_INVALID_ARG;
   for (const long long s : {(long long)x.q_token_stride, (long long)x.q_head_stride, (long long)x.o_token_stride,
                             (long long)x.o_head_stride})
@@ -896,7 +897,7 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   long long most = kt * rt;
   most = most > kTreeCtas ? kTreeCtas : most * x.cache.Hk;
   most = most > kTreeCtas ? kTreeCtas : most * x.cache.B;
-  const int ctas = (int)(most > kTreeCtas ? kTreeCtas : most);
+  const int ctas = (int)(most > kTreeCtas ? kTreeCtas : most < 1 ? 1 : most);       // (max_new 0: one, for the checks)
   const cudaStream_t s = static_cast<cudaStream_t>(x.stream);
   note_launches(0);
   const cudaError_t e = big ? launch_tree_big(tk, tv, a, fp8, fp16, ctas, s)

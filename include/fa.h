@@ -489,7 +489,9 @@ int fa_cache_keep(const fa_cache_keep_args* args);
  *   q       : in,  [total, Hq, d] (dtype), strides in elements, multiples of 8
  *   o       : out, [total, Hq, d] (dtype), strides likewise; lse : out, fp32 [total, Hq], dense
  *   max_new : at least every sequence's number of new tokens (a sequence with more is reported
- *             as FA_ERR_RANGE); it and Hq / Hk choose the kernel
+ *             as FA_ERR_RANGE); it and Hq / Hk choose the kernel.  0 says that no sequence has
+ *             any (all of the call's tokens are padding): nothing is written, and with workspace
+ *             NULL nothing is launched, so that the lengths are not checked either
  *   workspace : device scratch of fa_fwd_tree_workspace_bytes(total, Hq, Hk, d) bytes, 256-byte
  *               aligned, needs no initialisation; calls that may run at the same time need
  *               their own

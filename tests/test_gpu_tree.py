@@ -387,3 +387,25 @@ def test_units_that_end_anywhere_in_a_warp(d, dtype, fp8):
         o, lse = fa.attention_forward_tree(q, c.cache, c.cu, c.lens, T, tree_mask=bits)
         fa.fa_check_status()
         check_attention(c, q, o, lse, 1 / d ** 0.5, bits, f"T={T}", nan_ok=True)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_max_new_of_zero(fp8):
+    """It says that no sequence has new tokens: true for a batch that is all padding, whose results stay as they
+    were, and reported where a sequence has some."""
+    c = Case([20, 300], [2, 2], 2, 64, 16, BF, fp8, seed=3)
+    c.put(c.new(2), c.new(2))
+    q = c.new(4).cuda()
+    o, lse = torch.full_like(q, 7), torch.full((4, 4), 7.0, device="cuda")
+    empty = torch.full_like(c.cu, 4)
+    fa.attention_forward_tree(q, c.cache, empty, c.lens, 0, o=o, lse=lse)
+    fa.fa_check_status()
+    assert torch.all(o == 7) and torch.all(lse == 7)
+    for mask in (None, torch.zeros(4, 1, dtype=torch.int64, device="cuda")):
+        fa.attention_forward_tree(q, c.cache, c.cu, c.lens, 0, tree_mask=mask, o=o, lse=lse)
+        with pytest.raises(fa.FAError) as e:
+            fa.fa_check_status()
+        assert e.value.code == fa.FA_ERR_RANGE
+    fa.attention_forward_tree(q, c.cache, c.cu, c.lens, 2, o=o, lse=lse)
+    fa.fa_check_status()
+    check_attention(c, q, o, lse, 1 / 8)
