@@ -100,6 +100,13 @@ __device__ __forceinline__ int row_factor(float amax) {
   return ex == 255 ? 0 : max(-113, min(112, 127 + 14 - ex));
 }
 
+// Probabilities enter fp16 products as 2^15 times exp(s - max), the most that fp16 holds: then they have
+// its eleven bits down to 2^-29 of the largest (2^-14 without the factor), and what is below is off by at most
+// 2^-40 of it.  Many keys of small probability together count in a long context, and
+// without the factor those of 1.4 * 2^-24 were all 29 % off.  The row sum has the factor too, so it drops out of O; the running max is
+// kept less 15, so that max + log2(sum) is the LSE as before and parts merge as before.
+constexpr float kFp16Lift = 15.f;
+
 // ------------------------------------------------------------------------------------
 // Schedule of the attention over the cache.  A unit is one (sequence, key head, row tile): rows are
 // the unit's (new token, query head of the group) pairs.  Its keys are cut into chunks of 128 or 256.

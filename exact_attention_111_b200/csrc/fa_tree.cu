@@ -420,6 +420,7 @@ __global__ void __launch_bounds__(384, 1)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            if (!kFp8 && kMma16) mx -= kFp16Lift;
             float mn = fmaxf(m[nr][e], mx);
             if (kFp8 && mn <= m[nr][e] + 4.f) mn = m[nr][e];      // (-inf stays -inf only when both are)
             const float neg = mn == -INFINITY ? 0.f : -mn;

@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(512, 1)
                     const TreeArgs a) {
   using C = BigCfg<D, kFp8>;
   constexpr bool kMmaFp16 = kFp8 || kFp16;
+  constexpr float kLift = kMmaFp16 ? kFp16Lift : 0.f;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ BigShared sh;
   if ((smem_addr(smem_raw) & 1023u) != 0) {               // the tiles' swizzle needs it
@@ -719,7 +720,8 @@ __global__ void __launch_bounds__(512, 1)
         float sl2 = sl2q;
         // never 0, which would make NaN of a masked score's -inf
         if constexpr (kFp8) sl2 = fmaxf(sl2 * *reinterpret_cast<volatile float*>(&sh.kfac[(tile0 + u) & 7]), 0x1p-126f);
-        const float mx2 = row_max128(s) * sl2;
+        // m is the running max less kLift: the largest P is 2^kLift
+        const float mx2 = row_max128(s) * sl2 - kLift;
         float alpha = 1.f;
         if (mx2 > m) {
           alpha = ex2(m - mx2);                           // 0 when m = -inf
