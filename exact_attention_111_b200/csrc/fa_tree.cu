@@ -35,7 +35,6 @@ namespace fa {
 namespace {
 
 constexpr float kLn2f = 0.693147180559945309f;
-constexpr int kNoScale = -100000;        // no E yet: below every scale code
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -105,10 +104,11 @@ struct SmallCfg {
   static constexpr int kStages = 3 * 65536 / kStage;
   static constexpr int kRing = kStages * kStage;
   // Merge of the eight warps, eight rows at a time: each warp's O rows (a few floats apart beyond D, so
-  // that the fragments' stores spread over the banks), m and l of its rows, and E.
+  // that the fragments' stores spread over the banks), and its rows' statistics.
   static constexpr int kRowF = D + (kFp8 ? 2 : 4);
   static constexpr int kSlotF = 8 * kRowF;
-  static constexpr int kMerge = kRing, kStats = kMerge + 8 * kSlotF * 4, kBars = kStats + 8 * 16 * 4 + 8 * 4;
+  static constexpr int kStatF = kFp8 ? 24 : 16;           // of a warp: m, l and E4M3's reference of eight rows
+  static constexpr int kMerge = kRing, kStats = kMerge + 8 * kSlotF * 4, kBars = kStats + 8 * kStatF * 4;
   // E4M3: the chunks' scale codes, K's then V's
   static constexpr int kCodes = kBars + 2 * kStages * 8 + 16;
   static constexpr int kSmem = kCodes + (kFp8 ? kStages * 2 * kChunkKeys : 0);
@@ -131,13 +131,13 @@ __device__ __forceinline__ uint32_t swz(int r, int c, int panel) {
 }
 
 // kFp16: type of q and o.  A 16-bit cache's products are in that type.  An E4M3 cache's are in fp16, which
-// holds every code exactly: K's scale multiplies the score (32 bits), V's the probability before it
-// is rounded, p * 2^(e - E) with E a warp's own reference: 2^8 under the scales of its first keys,
-// moved (and O with it) when a scale is 2^11 above it.  So p * 2^(e - E) has fp16's full eleven
-// bits down to 2^-22 for keys of the usual scale, three more than bf16; and the running max may lag
-// by 2^4 before O is rescaled (p <= 2^4, p * 2^(e - E) <= 2^15): with few steps in a segment some
-// row's max grows in almost every one.  bf16 queries enter as fp16 with a power of two for each row
-// (row_factor).
+// holds every code exactly: K's scale 2^c multiplies the score (32 bits), V's goes into the key's weight,
+// 2^(s + c - R) with a reference R of each row's own, which follows the largest s + c that the row has seen: R
+// is moved (and O with it) when one is 2^15 above it, to 2^11 under it.  So weights have fp16's full eleven
+// bits down to 2^-25 of the row's largest, whatever the scales of other keys: R comes from visible keys
+// only.  (One reference for all rows, under the largest scale of a step, was one exponential a weight and
+// one maximum a row cheaper, but a scale 2^30 above the others, of a key that a row does not see or gives no
+// probability, left that row nothing.)  bf16 queries enter as fp16 with a power of two for each row (row_factor).
 template <int D, bool kFp8, bool kFp16, int kNR>
 __global__ void __launch_bounds__(384, 1)
     tree_small_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(384, 1)
       }
     }
     // O^T: columns r0 and r0 + 8 (E4M3: 2 r0 and 2 r0 + 1) of each 16, rows 2 tq, 2 tq + 1
-    float o[kNR][D / 16][4], m[kNR][2], l[kNR][2];
+    float o[kNR][D / 16][4], m[kNR][2], l[kNR][2], ref[kNR][2];
 #pragma unroll
     for (int nr = 0; nr < kNR; ++nr) {
 #pragma unroll
@@ -316,8 +316,8 @@ __global__ void __launch_bounds__(384, 1)
         for (int i = 0; i < 4; ++i) o[nr][n][i] = 0.f;
       m[nr][0] = m[nr][1] = -INFINITY;
       l[nr][0] = l[nr][1] = 0.f;
+      ref[nr][0] = ref[nr][1] = -INFINITY;                // E4M3: R; otherwise O's reference is m
     }
-    int eref = kNoScale;                                  // E4M3: E (as a scale code) of what O holds
 
     // ------------------------------------------------------------ the segment's steps
     // Unit, sequence and head stay; only kt moves until the unit or the part ends.
@@ -340,7 +340,7 @@ __global__ void __launch_bounds__(384, 1)
           for (int g = 0; g < kG; ++g)
 #pragma unroll
             for (int i = 0; i < 4; ++i) sc[nr][g][i] = 0.f;
-        float kf[kG][2], vf[kG][2];
+        float kf[kG][2], vf[kG][2];                       // K's scales, V's exponents
         const int lrow = (lane & 7) + ((lane >> 3) & 1) * 8, lchunk = lane >> 4;
         if constexpr (kFp8) {
 #pragma unroll
@@ -357,24 +357,9 @@ __global__ void __launch_bounds__(384, 1)
                 for (int nr = 0; nr < kNR; ++nr) mma16816<true>(sc[nr][g], af, qf[nr][c + i][0], qf[nr][c + i][1]);
               }
             }
-          // the largest of V's scales (0 where no key is)
           const int ck = smem_raw[C::kCodes + us * 2 * C::kChunkKeys + key0 + lane];
           const int cv = smem_raw[C::kCodes + (us * 2 + 1) * C::kChunkKeys + key0 + lane];
-          const int top = (int)__reduce_max_sync(0xffffffffu, (unsigned)cv);
-          if (top > eref + 11) {
-            const int e = top - 8;
-            if (eref != kNoScale) {                       // rare: a scale far above the ones before
-              const float f = exp2f((float)(eref - e));
-#pragma unroll
-              for (int nr = 0; nr < kNR; ++nr)
-#pragma unroll
-                for (int n = 0; n < D / 16; ++n)
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) o[nr][n][i] *= f;
-            }
-            eref = e;
-          }
-          const float fk = scale_value(ck), fv = scale_value(max(cv + 127 - eref, 0));
+          const float fk = scale_value(ck), fv = (float)(cv - 127);
 #pragma unroll
           for (int g = 0; g < kG; ++g)
 #pragma unroll
@@ -421,8 +406,7 @@ __global__ void __launch_bounds__(384, 1)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             if (!kFp8 && kMma16) mx -= kFp16Lift;
-            float mn = fmaxf(m[nr][e], mx);
-            if (kFp8 && mn <= m[nr][e] + 4.f) mn = m[nr][e];      // (-inf stays -inf only when both are)
+            const float mn = fmaxf(m[nr][e], mx);
             const float neg = mn == -INFINITY ? 0.f : -mn;
             const float al = ex2(m[nr][e] + neg);         // 0 while m = -inf
             m[nr][e] = mn;
@@ -433,14 +417,36 @@ __global__ void __launch_bounds__(384, 1)
               for (int i = 0; i < 2; ++i) {
                 const float p = ex2(x[g][i] + neg);
                 sum += p;
-                sc[nr][g][2 * i + e] = kFp8 ? p * vf[g][i] : p;
+                sc[nr][g][2 * i + e] = p;
               }
             l[nr][e] = l[nr][e] * al + sum;
-            if (__any_sync(0xffffffffu, al != 1.f)) {
+            float ol = al;                                // O's rescale
+            if constexpr (kFp8) {
+#pragma unroll
+              for (int g = 0; g < kG; ++g)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) x[g][i] += vf[g][i];
+              float my = fmaxf(x[0][0], x[0][1]);
+#pragma unroll
+              for (int g = 1; g < kG; ++g) my = max3f(my, x[g][0], x[g][1]);
+              my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 4));
+              my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 8));
+              my = fmaxf(my, __shfl_xor_sync(0xffffffffu, my, 16));
+              const float rn = my > ref[nr][e] + 15.f ? my - 11.f : ref[nr][e];
+              const float nref = rn == -INFINITY ? 0.f : -rn;
+              ol = ex2(ref[nr][e] + nref);
+              if (rn == ref[nr][e]) ol = 1.f;             // (-inf as well: O is zero)
+              ref[nr][e] = rn;
+#pragma unroll
+              for (int g = 0; g < kG; ++g)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) sc[nr][g][2 * i + e] = ex2(x[g][i] + nref);
+            }
+            if (__any_sync(0xffffffffu, ol != 1.f)) {
 #pragma unroll
               for (int n = 0; n < D / 16; ++n) {
-                o[nr][n][e] *= al;
-                o[nr][n][2 + e] *= al;
+                o[nr][n][e] *= ol;
+                o[nr][n][2 + e] *= ol;
               }
             }
           }
@@ -560,8 +566,7 @@ __global__ void __launch_bounds__(384, 1)
       a.meta[2 * blockIdx.x + 1] = make_int4(row0, 0, 0, 0);
     }
     float* so = reinterpret_cast<float*>(smem_raw + C::kMerge) + warp * C::kSlotF;
-    float* stats = reinterpret_cast<float*>(smem_raw + C::kStats);       // [warp][m of 8 rows, l of 8 rows]
-    int* es = reinterpret_cast<int*>(stats + 8 * 16);
+    float* stats = reinterpret_cast<float*>(smem_raw + C::kStats);       // [warp][m of 8 rows, l of 8 rows, R of 8 rows]
 #pragma unroll
     for (int nr = 0; nr < kNR; ++nr) {
         const int rb = nr * 8;
@@ -586,29 +591,28 @@ __global__ void __launch_bounds__(384, 1)
             }
           }
           if (r0 == 0) {
-            stats[warp * 16 + 2 * tq + e] = m[nr][e];
-            stats[warp * 16 + 8 + 2 * tq + e] = l[nr][e];
+            stats[warp * C::kStatF + 2 * tq + e] = m[nr][e];
+            stats[warp * C::kStatF + 8 + 2 * tq + e] = l[nr][e];
+            if constexpr (kFp8) stats[warp * C::kStatF + 16 + 2 * tq + e] = ref[nr][e];
           }
         }
-        if (kFp8 && lane == 0) es[warp] = eref;
         named_bar_sync(1, 256);
         const int r = rb + warp;
         if (r < nrows) {
           constexpr int kV = D / 32;                      // columns of a lane
-          float mr = -INFINITY;
-          int er = kNoScale;
+          float mr = -INFINITY, rr = -INFINITY;
 #pragma unroll
           for (int w = 0; w < 8; ++w) {
-            mr = fmaxf(mr, stats[w * 16 + warp]);
-            if constexpr (kFp8) er = max(er, es[w]);
+            mr = fmaxf(mr, stats[w * C::kStatF + warp]);
+            if constexpr (kFp8) rr = fmaxf(rr, stats[w * C::kStatF + 16 + warp]);
           }
-          const float neg = mr == -INFINITY ? 0.f : -mr;
+          const float neg = mr == -INFINITY ? 0.f : -mr, nrr = rr == -INFINITY ? 0.f : -rr;
           float lr = 0.f, x[kV] = {};
 #pragma unroll
           for (int w = 0; w < 8; ++w) {
-            float f = ex2(stats[w * 16 + warp] + neg);
-            lr += f * stats[w * 16 + 8 + warp];
-            if constexpr (kFp8) f *= exp2f((float)(es[w] - er));
+            float f = ex2(stats[w * C::kStatF + warp] + neg);
+            lr += f * stats[w * C::kStatF + 8 + warp];
+            if constexpr (kFp8) f = ex2(stats[w * C::kStatF + 16 + warp] + nrr);
             const float* src = reinterpret_cast<const float*>(smem_raw + C::kMerge) + w * C::kSlotF + warp * C::kRowF + lane * kV;
 #pragma unroll
             for (int i = 0; i < kV; i += 2) {
@@ -617,10 +621,13 @@ __global__ void __launch_bounds__(384, 1)
               x[i + 1] += f * v.y;
             }
           }
-          // what O is a multiple of: 2^(E - 127)
-          const float vref = kFp8 && er != kNoScale ? exp2f((float)(er - 127)) : 1.f;
+          if constexpr (kFp8) {                           // O's reference from R to m, 2^(R - m) in two steps: it
+            const float f = rr == -INFINITY ? 0.f : ex2(0.5f * (rr + neg));        // may lie outside fp32's normal range
+#pragma unroll
+            for (int i = 0; i < kV; ++i) x[i] = x[i] * f * f;
+          }
           if (whole) {
-            const float inv = lr == 0.f ? 0.f : vref / lr;
+            const float inv = lr == 0.f ? 0.f : 1.f / lr;
             const int t = (row0 + r) / a.G, g = (row0 + r) - t * a.G;
             const long long tk = s.cu0 + t;
             const int hq = h * a.G + g;
@@ -633,7 +640,7 @@ __global__ void __launch_bounds__(384, 1)
             if (lane == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(mr, lr);
 #pragma unroll
             for (int i = 0; i < kV; i += 2)
-              *reinterpret_cast<float2*>(a.part_o + at * D + lane * kV + i) = make_float2(x[i] * vref, x[i + 1] * vref);
+              *reinterpret_cast<float2*>(a.part_o + at * D + lane * kV + i) = make_float2(x[i], x[i + 1]);
           }
         }
       }

@@ -1,15 +1,18 @@
-"""GPU: attention over the cache where the weights of the visible keys lie far apart: many small weights
-beside a large one.
+"""GPU: attention over the cache where the weights of the visible keys, or the E4M3 scales of the keys, lie far
+apart: many small weights beside a large one; keys a row does not see, or gives no weight, of any size.
 
-The bound of tests/paged.py allows 2^-25 of sum |v|, what P in fp16 loses when its largest is 1.  Here the
-kernels are held to what they promise: weights keep the 16-bit type's own bits down to far below the
-largest.  For each row, with p the true weights (they sum to 1) and sums over the visible keys only,
+The bound of tests/paged.py allows 2^-25 of sum |v|, what P in fp16 loses when its largest is 1, and of keys that
+all rows see.  Here the kernels are held to what they promise: weights keep the 16-bit type's own bits down to
+far below the row's largest.  For each row, with p the true weights (they sum to 1), v_j = code_j * 2^e_j (e_j = 0 in
+a 16-bit cache) and sums over the visible keys only,
 
-    |dO| <= (u + 2 ds) sum p |v| + u (1 + u) |O| + 2^-40 max(p) sum |v| + 2^-126,
+    |dO| <= (u + 2 ds) sum p |v| + u (1 + u) |O| + w max_j(p_j 2^e_j) sum_j |code_j| + 2^-126,
 
-u half a step of the 16-bit type, ds = 2^-16 (R + 1) the scores' error as there.  The third term: P's largest is
-2^15, and below 2^-14 fp16 is off by 2^-25, 2^-40 of the largest.  The last term is what fp32 resolves;
-a result below fp16's normal range is off by 2^-25 itself."""
+u half a step of the 16-bit type, ds = 2^-16 (R + 1) the scores' error as there.  The third term: in a 16-bit cache
+P's largest is 2^15, and below 2^-14 fp16 is off by 2^-25, so w = 2^-40.  E4M3 weights p_j 2^e_j have a largest of
+2^11 at least, which gives 2^-36; 128 keys whose scales are all within 2^8 may share a reference, which then
+lies up to 2^8 above the row's own largest: w = 2^-28.  The last term is what fp32 resolves; a result below
+fp16's normal range is off by 2^-25 itself."""
 
 from __future__ import annotations
 
@@ -25,8 +28,9 @@ pytestmark = pytest.mark.gpu
 BF, HF = torch.bfloat16, torch.float16
 
 
-def exact(q, k, v, see, scale):
-    """fp64 on the GPU: q [T, Hq, d], k, v [Hk, n, d], see [T, n].  O, LSE, sum p |v|, max(p) sum |v| and R."""
+def exact(q, k, v, see, scale, e=None):
+    """fp64 on the GPU: q [T, Hq, d], k, v [Hk, n, d], see [T, n], e [Hk, n].  O, LSE, sum p |v|, the third term's
+    max times sum, and R."""
     T, Hq, d = q.shape
     G = Hq // k.shape[0]
     q = q.double()
@@ -34,25 +38,29 @@ def exact(q, k, v, see, scale):
     lse, r = (torch.zeros(T, Hq, dtype=torch.float64, device=q.device) for _ in range(2))
     for h in range(Hq):
         kk, vv = k[h // G].double(), v[h // G].double()
+        size = torch.ones_like(vv[:, 0]) if e is None else torch.exp2(e[h // G].double())
         for t in range(T):                               # visible keys only: the others may hold anything
             i = see[t].nonzero()[:, 0]
             s = scale * (kk[i] @ q[t, h])
             lse[t, h] = torch.logsumexp(s, 0)
             p = torch.exp(s - lse[t, h])
-            o[t, h], a[t, h], low[t, h] = p @ vv[i], p @ vv[i].abs(), p.max() * vv[i].abs().sum(0)
+            o[t, h], a[t, h] = p @ vv[i], p @ vv[i].abs()
+            low[t, h] = (p * size[i]).max() * (vv[i].abs() / size[i][:, None]).sum(0)
             r[t, h] = (scale * (kk[i].abs() @ q[t, h].abs())).max()
     return o, lse, a, low, r
 
 
-def check(q, o, lse, want, label=""):
+def check(q, o, lse, want, w=2.0 ** -40, label="", rows=None):
     u = float(torch.finfo(q.dtype).eps) / 2
-    ro, rl, a, low, r = want
+    rows = slice(None) if rows is None else rows
+    o, lse = o[rows], lse[rows]
+    ro, rl, a, low, r = (x[rows] for x in want)
     ds = 2.0 ** -16 * (r + 1)
     assert torch.isfinite(o).all() and torch.isfinite(lse).all(), f"{label}: not finite"
     dl = (lse.double() - rl).abs() - (ds + 2.0 ** -20 * (1 + rl.abs()))
     assert float(dl.max()) <= 0, f"{label}: lse over its bound by {float(dl.max())}"
     d = (o.double() - ro).abs()
-    bound = (u + 2 * ds[..., None]) * a + u * (1 + u) * ro.abs() + 2.0 ** -40 * low + 2.0 ** -126
+    bound = (u + 2 * ds[..., None]) * a + u * (1 + u) * ro.abs() + w * low + 2.0 ** -126
     bound = bound + (2.0 ** -25 if q.dtype is HF else 0.0)
     over = (d / bound).max()
     assert float(over) <= 1, f"{label}: {float(over)} times the bound (off by {float(d.max())})"
@@ -80,4 +88,119 @@ def test_many_small_weights_beside_a_large_one(dtype, n, down):
     o, lse = fa.attention_forward_tree(q, cache, cu, lens, n)
     fa.fa_check_status()
     see = torch.arange(N + n, device="cuda")[None] <= N + torch.arange(n, device="cuda")[:, None]
-    check(q, o, lse, exact(q, *(x.view(1, -1, d)[:, :N + n] for x in (k, v)), see, d ** -0.5), f"2^-{down}")
+    check(q, o, lse, exact(q, *(x.view(1, -1, d)[:, :N + n] for x in (k, v)), see, d ** -0.5), label=f"2^-{down}")
+
+
+class Filled:
+    """An E4M3 cache of one sequence, written from k, v [N, Hk, d]; what it holds in fp64."""
+
+    def __init__(self, k, v, page=16):
+        ensure_built()
+        N, Hk, d = k.shape
+        pages = -(-N // page)
+        g = torch.Generator().manual_seed(N)
+        order = torch.randperm(pages, generator=g).to(device="cuda", dtype=torch.int32)
+        codes = [torch.full((pages, Hk, page, d), 127, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        scales = [torch.full((pages, Hk, page), 200, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        self.cache = fa.KVCache(*codes, order[None].contiguous(), *scales)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        fa.cache_append(self.cache, k.to(BF).cuda(), v.to(BF).cuda(), torch.tensor([0, N], **i32), torch.zeros(1, **i32))
+        at = order.long()
+
+        def dense(x):
+            return x[at].transpose(0, 1).flatten(1, 2)[:, :N]
+
+        self.k, self.v = (dense(c.view(torch.float8_e4m3fn)).double() * torch.exp2(dense(s).double() - 127)[..., None]
+                          for c, s in zip(codes, scales))
+        self.e = dense(scales[1]).double() - 127
+        self.N, self.d = N, d
+
+    def attend(self, q, n, mask=None, unseen=()):
+        """The last n tokens attend: checks the rows that see none of the new tokens `unseen`."""
+        i32 = dict(dtype=torch.int32, device="cuda")
+        L = self.N - n
+        o, lse = fa.attention_forward_tree(q, self.cache, torch.tensor([0, n], **i32), torch.tensor([L], **i32), n,
+                                           tree_mask=mask)
+        fa.fa_check_status()
+        see = torch.ones(n, self.N, dtype=torch.bool, device="cuda")
+        j = torch.arange(n, device="cuda")
+        see[:, L:] = j[None] <= j[:, None] if mask is None else (mask[:, :1] >> j[None] & 1).bool()
+        rows = ~see[:, [L + t for t in unseen]].any(1)
+        assert rows.any()
+        check(q, o, lse, exact(q, self.k, self.v, see, self.d ** -0.5, self.e), 2.0 ** -28, rows=rows)
+
+
+def _rows(N, seed, heads=2, d=64):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(N, heads, d, generator=g)
+
+
+@pytest.mark.parametrize("n", [2, 8])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("tree", [False, True])
+@pytest.mark.parametrize("which,up", [("v", 12), ("v", 24), ("v", 34), ("v", 60), ("v", 120), ("k", 17), ("k", 25), ("k", 40),
+                                      ("k", 60), ("k", 120), ("kv", 30), ("kv", -40)])
+def test_finite_keys_a_row_does_not_see_do_not_reach_it(which, up, dtype, tree, n):
+    """Later tokens of a chain and siblings of a tree whose rows are 2^up times as large."""
+    N = 200 + n
+    k, v = _rows(N, 1), _rows(N, 2)
+    big = [n - 1] if n < 20 else [n - 1, 20]
+    for t in big:
+        for x in ([k] if "k" in which else []) + ([v] if "v" in which else []):
+            x[200 + t] *= 2.0 ** up
+    c = Filled(k, v)
+    mask = None
+    if tree:                                             # a star: siblings do not see one another
+        mask = fa.tree_mask([-1] + [0] * (n - 1), torch.tensor([0, n], device="cuda"))
+    c.attend(_rows(n, 3, 4).to(dtype).cuda(), n, mask, big)
+
+
+@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("up", [12, 24, 40, 60])
+@pytest.mark.parametrize("where", [0, 130, 199])
+def test_large_values_of_no_weight(dtype, n, up, where):
+    """Keys that all rows see, of values 2^up times as large and weights some 2^-(up + 30) as large."""
+    N = 200 + n
+    k, v, q = _rows(N, 1), _rows(N, 2), _rows(n, 3, 4)
+    q[..., 0], k[..., 0] = 8.0, 0.0
+    k[where] = 0
+    k[where, :, 0] = -(up + 30) * float(np.log(2))
+    v[where] *= 2.0 ** up
+    Filled(k, v).attend(q.to(dtype).cuda(), n)
+
+
+@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("up", [17, 25, 40, 100])
+def test_large_keys_across_the_queries(dtype, n, up):
+    """Keys that are 2^up times as large as the others in a column where the queries are zero."""
+    N = 200 + n
+    k, v, q = _rows(N, 1), _rows(N, 2), _rows(n, 3, 4)
+    q[..., 5] = 0
+    k[..., 5] = 0
+    for where in (3, 131, 198):
+        k[where] = 0
+        k[where, :, 5] = 2.0 ** up
+    Filled(k, v).attend(q.to(dtype).cuda(), n)
+
+
+@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("step", [-30, -9, 9, 30])
+def test_values_that_grow_or_fall_along_the_keys(dtype, n, step):
+    """Each 64 keys' values are 2^step times those before, and the queries weigh only one block: each in turn."""
+    N = 320 + n
+    k, v = _rows(N, 1), _rows(N, 2)
+    q = _rows(n, 3, 4)
+    for b in range(5):
+        v[64 * b:64 * b + 64] *= 2.0 ** (step * (b - 2))
+    v[320:] *= 2.0 ** (-3 * abs(step))
+    for b in range(5):
+        kb = k.clone()
+        kb[..., 0], q[..., 0] = 0.0, 8.0
+        kb[:, :, 0] = -100.0
+        kb[64 * b:64 * b + 64, :, 0] = 0.0
+        if dtype is HF and step * (b - 2) > 12:
+            continue                                     # not a result that fp16 holds
+        Filled(kb, v).attend(q.to(dtype).cuda(), n)
