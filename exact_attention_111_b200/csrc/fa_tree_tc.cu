@@ -106,23 +106,27 @@ struct BigShared {
   // publishes after it has read entry n.
   int odd[2][2];
   float alpha[2][kTile];
-  // E4M3: staged scale codes of a tile (K's and V's with K, V's with V), and by tile mod 8 the factors of its K, of what O
-  // holds and of O.  Entry u is written again for tile u + 8, whose K slot is free only
+  // E4M3: staged scale codes of a tile (K's and V's with K, V's with V), and by tile mod 8 2^E of its K and E of its V
+  // (kfac 0, vexp kWide: rows as they are).  Entry u is written again for tile u + 8, whose K slot is free only
   // after S of tile u + 8 - kStages, so of u + 4, which waited for both softmax groups to have finished u + 3.
   alignas(16) uint8_t scales[3][kTile];
-  float kfac[8], vfac[8], vref[8];
+  float kfac[8], vexp[8];
   Walk walk[8];                  // one per softmax warp, whose registers are full
 };
 
 // Whether tile kt holds new tokens or reaches past them.
 __device__ __forceinline__ bool tail_tile(const Seg& e, int kt) { return (kt + 1) * kChunk > e.s.len; }
 
-// E4M3 rows enter the fp16 products as code * 2^(scale - E): a code is exact in fp16, and with E the
-// largest scale of the tile's keys what a row of a much smaller scale loses is below 2^-25 of the
-// largest, far under the products' own rounding.  K: E is the tile's, its 2^E goes into the
-// tile's score factor.  V: O adds up tiles, so E stays the segment's (its first tile's) while later
-// tiles' scales are at most 2^7 larger (448 * 2^7 is the last that fp16 holds); one that is larger
-// becomes E, and what O holds is scaled down with the softmax's own rescale.
+// E4M3 rows enter the fp16 products as code * 2^(scale - E) with E the largest scale of the tile's keys, exactly:
+// a code has its last bit at 2^-9, fp16 at 2^-24, so scales may be 2^15 apart (K) and are let to be 2^8 apart (V).
+// 2^E of K goes into the tile's score factor; E of V into the exponent of the weights, 2^(s + E - R), with a
+// reference R of each row's own, which follows the largest max(s) + E of the row's tiles (visible keys only): R is
+// moved (and O with it) when one is 2^15 above it, to 2^11 under it.  Weights keep fp16's eleven bits down to 2^-25
+// of the row's largest, or 2^-17 where a tile puts R too high by a key of up to 2^8 the size that the row
+// does not see.  A tile whose scales are further apart ("wide") keeps its rows as they are, and the softmax takes each key's scale
+// from the cache, K's to the score and V's to the weight, so that no key's size depends on another's.
+// Rows of scale code 0 or 1 (zeros, and values below 2^-117) do not make a tile wide; they become zero beside
+// others 2^25 as large.
 //
 // Warp 12 keeps one tile's codes of K and of V ahead in shared memory by TMA.  Warps 14 and 15 expand
 // K into the ring; the correction warps expand V, one tile ahead of their rescales.  In tiles that hold
@@ -134,22 +138,30 @@ __device__ __forceinline__ uint32_t half2_pow2(int d) {
   return h | (h << 16);
 }
 
-// The largest of a tile's first `keys` scale codes; one warp.
-__device__ __forceinline__ uint32_t top_scale(const uint8_t* scales, int keys) {
+constexpr float kWide = 1000.f;          // vexp of a wide tile
+constexpr int kRaw = -1000;              // expand_tile: rows as they are
+
+// The largest of a tile's first `keys` scale codes, and whether the smallest above 1 is more than `apart` below; one warp.
+__device__ __forceinline__ uint32_t top_scale(const uint8_t* scales, int keys, uint32_t apart, bool& wide) {
   const int lane = lane_id(), k = keys - 4 * lane;
   uint32_t x = *reinterpret_cast<const uint32_t*>(scales + 4 * lane);
   x &= k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
-  return __reduce_max_sync(0xffffffffu, max(max(x & 0xFF, (x >> 8) & 0xFF), max((x >> 16) & 0xFF, x >> 24)));
+  uint32_t top = 0, low = 255;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t b = (x >> (8 * i)) & 0xFF;
+    top = max(top, b);
+    low = min(low, b > 1 ? b : 255u);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  wide = __any_sync(0xffffffffu, low + apart < top);
+  return top;
 }
-
-// E of V after a tile whose largest scale is ev.
-__device__ __forceinline__ uint32_t next_eref(uint32_t eref, uint32_t ev, bool first) {
-  return first || ev > eref + 7 ? ev : eref;
-}
+constexpr uint32_t kApartK = 15, kApartV = 8;
 
 // Expand one tile (128 rows of D codes, as TMA staged them) into a ring tile: warp wi of nW.  A pass
 // of a warp is 32 / kLanes rows; row factors are computed once, two or one per lane, and
-// shuffled.  clean (V): rows from `keys` on become zero and NaN codes too; returns whether there were.
+// shuffled (e = kRaw: 1).  clean (V): rows from `keys` on become zero and NaN codes too; returns whether there were.
 // The caller releases the staging behind the stores and the proxy fence.  (Released behind the last loads,
 // before their values were used, the next copy got in first: whole V tiles came out wrong.)
 template <int D, int nW>
@@ -162,7 +174,7 @@ __device__ __forceinline__ bool expand_tile(const uint8_t* src0, uint8_t* dst0, 
 #pragma unroll
   for (int k = 0; k < kF; ++k) {
     const int j = k * 32 + lane;
-    f[k] = half2_pow2((int)scales[(j / kW) * (nW * kW) + wi * kW + j % kW] - e);
+    f[k] = e == kRaw ? half2_pow2(0) : half2_pow2((int)scales[(j / kW) * (nW * kW) + wi * kW + j % kW] - e);
   }
   bool odd = false;
   // chunk `chunk` of the codes (16) is chunks 2 chunk, 2 chunk + 1 of the row (8 values each); at d =
@@ -296,7 +308,6 @@ __device__ void expand_k_role(const TreeArgs& a, BigShared& sh, uint8_t* sK, con
   volatile int* abort_flag = &sh.abort_flag;
   const Seg& e = w.e;
   int n = 0;
-  uint32_t eref = 0;
   bool ok = true;
   while (ok && w.next(a)) {
     for (int u = 0; u < e.nu && ok; ++u, ++n) {
@@ -306,15 +317,14 @@ __device__ void expand_k_role(const TreeArgs& a, BigShared& sh, uint8_t* sK, con
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       const int keys = e.s.len + e.s.T - (e.kt0 + u) * kChunk;
-      const uint32_t ek = top_scale(sh.scales[0], keys);
-      const uint32_t en = next_eref(eref, top_scale(sh.scales[1], keys), u == 0);
+      bool wide_k, wide_v;
+      const uint32_t ek = top_scale(sh.scales[0], keys, kApartK, wide_k);
+      const uint32_t ev = top_scale(sh.scales[1], keys, kApartV, wide_v);
       if (wi == 0 && lane == 0) {
-        *reinterpret_cast<volatile float*>(&sh.kfac[n & 7]) = scale_value(ek);
-        *reinterpret_cast<volatile float*>(&sh.vfac[n & 7]) = u == 0 ? 1.f : exp2f((float)eref - (float)en);
-        *reinterpret_cast<volatile float*>(&sh.vref[n & 7]) = scale_value(en);
+        *reinterpret_cast<volatile float*>(&sh.kfac[n & 7]) = wide_k ? 0.f : scale_value(ek);
+        *reinterpret_cast<volatile float*>(&sh.vexp[n & 7]) = wide_v ? kWide : (float)((int)ev - 127);
       }
-      eref = en;
-      expand_tile<D, 2>(sC, sK + s * (kTile * D * 2), sh.scales[0], (int)ek, wi, false, 0);
+      expand_tile<D, 2>(sC, sK + s * (kTile * D * 2), sh.scales[0], wide_k ? kRaw : (int)ek, wi, false, 0);
       fence_async_smem();
       mbar_arrive(&sh.k_full[s]);
       mbar_arrive(&sh.c_empty[0]);
@@ -341,6 +351,79 @@ __device__ __forceinline__ float row_to_fp16(uint32_t* x) {
   return scale_value(127 - k);
 }
 
+// The scale codes of keys pos .. pos + 15 (zeros where there is no key, or no page).
+__device__ __forceinline__ void load_codes(const TreeArgs& a, const Seg& e, int pos, uint4& ks, uint4& vs) {
+  ks = vs = make_uint4(0, 0, 0, 0);
+  if (pos >= e.s.len + e.s.T) return;
+  const long long row = slot_row(a.c, e.b, e.h, pos);
+  if (row < 0) return;
+  ks = *reinterpret_cast<const uint4*>(a.c.ks + row);
+  vs = *reinterpret_cast<const uint4*>(a.c.vs + row);
+}
+__device__ __forceinline__ uint32_t byte_of(const uint4& w, int i) {
+  const uint32_t x = i < 4 ? w.x : i < 8 ? w.y : i < 12 ? w.z : w.w;
+  return (x >> (8 * (i & 3))) & 0xFF;
+}
+
+// One row's softmax of an E4M3 tile in its general form: for a wide tile (kf 0: the scores lack K's scales; ve kWide:
+// V's rows lack theirs), and where R and m are so far apart that the row sum needs exponentials of its
+// own.  Rare and slow: scale codes come from the cache, each weight takes two exponentials, and the scores are read
+// from tensor memory twice, 32 at a time, so that the usual path keeps its registers.  (P goes over
+// scores that have been read: columns 16 h of 32 h.)
+__device__ __forceinline__ void wide_tile(const TreeArgs& a, const Seg& e, int t, int kt, float sl2q, float kf, float ve,
+                                          uint32_t tS, float& m, float& l, float& ref, float* alpha, uint64_t* alpha_full) {
+  uint32_t s[32];                                         // 32 scores, masked and scaled
+  float c[32];                                            // the keys' V exponents
+  auto load = [&](int h) {
+    __syncwarp();
+    tmem_ld32_sync(tS + 32 * h, s);
+    const uint32_t vis = visible32(a, e.s, t, kt * kChunk + 32 * h - e.s.len);
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+      uint4 ks, vs;
+      load_codes(a, e, kt * kChunk + 32 * h + 16 * g, ks, vs);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const int j = 16 * g + i;
+        const float x = __uint_as_float(s[j]) * (sl2q * (kf == 0.f ? scale_value(byte_of(ks, i)) : kf));
+        s[j] = __float_as_uint((vis >> j) & 1u ? x : -INFINITY);
+        c[j] = ve == kWide ? (float)((int)byte_of(vs, i) - 127) : ve;
+      }
+    }
+  };
+  float mx = -INFINITY, my = -INFINITY;
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h) {
+    load(h);
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      mx = fmaxf(mx, __uint_as_float(s[j]));
+      my = fmaxf(my, __uint_as_float(s[j]) + c[j]);
+    }
+  }
+  const float mn = fmaxf(m, mx), rn = my > ref + 15.f ? my - 11.f : ref;
+  l *= mn == -INFINITY ? 1.f : ex2(m - mn);
+  m = mn;
+  *alpha = rn == ref ? 1.f : ex2(ref - rn);
+  ref = rn;
+  mbar_arrive(alpha_full);
+  const float mneg = m == -INFINITY ? 0.f : -m, rneg = ref == -INFINITY ? 0.f : -ref;
+#pragma unroll 1
+  for (int h = 0; h < 4; ++h) {
+    load(h);
+    uint32_t pk[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      const float x = __uint_as_float(s[2 * i]), y = __uint_as_float(s[2 * i + 1]);
+      l += ex2(x + mneg) + ex2(y + mneg);
+      pk[i] = pack2<true>(ex2(x + c[2 * i] + rneg), ex2(y + c[2 * i + 1] + rneg));
+    }
+    __syncwarp();                                         // the store is the whole warp's
+    tmem_st16(tS + 16 * h, pk);
+    tmem_wait_st();
+  }
+}
+
 // kFp16: type of q and o.  The products of a 16-bit cache are in that type, those of an E4M3 cache in fp16.
 template <int D, bool kFp8, bool kFp16>
 __global__ void __launch_bounds__(512, 1)
@@ -348,7 +431,7 @@ __global__ void __launch_bounds__(512, 1)
                     const TreeArgs a) {
   using C = BigCfg<D, kFp8>;
   constexpr bool kMmaFp16 = kFp8 || kFp16;
-  constexpr float kLift = kMmaFp16 ? kFp16Lift : 0.f;
+  constexpr float kLift = kFp16 ? kFp16Lift : 0.f;      // 16-bit caches (an E4M3 cache's weights have a reference)
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   __shared__ BigShared sh;
   if ((smem_addr(smem_raw) & 1023u) != 0) {               // the tiles' swizzle needs it
@@ -557,7 +640,6 @@ __global__ void __launch_bounds__(512, 1)
     Walk w;
     w.start(part);
     const Seg& e = w.e;
-    uint32_t eref = 0;
     while (ok && w.next(a)) {
       const int nq = e.nrows > kTile ? 2 : 1;
       auto expand_v = [&](int u) -> bool {                // tile u of the segment
@@ -566,8 +648,9 @@ __global__ void __launch_bounds__(512, 1)
         if (go && n >= C::kStages) go = mbar_wait(&sh.v_empty[s], ((n / C::kStages) - 1) & 1, abort_flag, st);
         if (!__all_sync(0xffffffffu, go)) return false;
         const int keys = e.s.len + e.s.T - (e.kt0 + u) * kChunk;
-        eref = next_eref(eref, top_scale(sh.scales[2], keys), u == 0);
-        if (expand_tile<D, 4>(sC + C::kCodes, sV + s * C::kTileBytes, sh.scales[2], (int)eref, wq,
+        bool wide;
+        const uint32_t ev = top_scale(sh.scales[2], keys, kApartV, wide);
+        if (expand_tile<D, 4>(sC + C::kCodes, sV + s * C::kTileBytes, sh.scales[2], wide ? kRaw : (int)ev, wq,
                               tail_tile(e, e.kt0 + u), keys))
           for (int q = 0; q < nq; ++q) *reinterpret_cast<volatile int*>(&sh.odd[q][seg[q] & 1]) = seg[q] + 1;
         fence_async_smem();
@@ -674,7 +757,7 @@ __global__ void __launch_bounds__(512, 1)
       const bool live = r < e.nrows;
       const int R = e.row0 + (live ? r : 0);
       const int t = R / a.G;
-      float sl2q = a.scale_log2, vref = 1.f;
+      float sl2q = a.scale_log2;
       if (e.nu > 0) {
         // Q row into the swizzled tile (rows without a token: zeros)
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (e.s.cu0 + t) * a.q_tok + (e.h * a.G + (R - t * a.G)) * a.q_head);
@@ -690,7 +773,7 @@ __global__ void __launch_bounds__(512, 1)
         tc_fence_before();
         mbar_arrive(&sh.q_full[q]);
       }
-      float m = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f, ref = -INFINITY;      // ref: R, with an E4M3 cache
       for (int u = 0; u < e.nu; ++u) {
         const int kt = e.kt0 + u;
         ok = mbar_wait(&sh.s_full[q], cs & 1, abort_flag, st);
@@ -717,24 +800,38 @@ __global__ void __launch_bounds__(512, 1)
               if (!((vis >> i) & 1u)) s[32 * h + i] = -INFINITY;
           }
         }
-        float sl2 = sl2q;
-        // never 0, which would make NaN of a masked score's -inf
-        if constexpr (kFp8) sl2 = fmaxf(sl2 * *reinterpret_cast<volatile float*>(&sh.kfac[(tile0 + u) & 7]), 0x1p-126f);
-        // m is the running max less kLift: the largest P is 2^kLift
-        const float mx2 = row_max128(s) * sl2 - kLift;
-        float alpha = 1.f;
-        if (mx2 > m) {
-          alpha = ex2(m - mx2);                           // 0 when m = -inf
-          m = mx2;
-        }
+        float sl2 = sl2q, alpha = 1.f, mneg, lfac = 1.f;
         if constexpr (kFp8) {
-          sh.alpha[q][rl] = alpha * *reinterpret_cast<volatile float*>(&sh.vfac[(tile0 + u) & 7]);
-          vref = *reinterpret_cast<volatile float*>(&sh.vref[(tile0 + u) & 7]);
+          const float kf = *reinterpret_cast<volatile float*>(&sh.kfac[(tile0 + u) & 7]);
+          const float ve = *reinterpret_cast<volatile float*>(&sh.vexp[(tile0 + u) & 7]);
+          sl2 = fmaxf(sl2q * kf, 0x1p-126f);              // never 0, which would make NaN of a masked score's -inf
+          const float mx2 = row_max128(s) * sl2;
+          const float mn = fmaxf(m, mx2), rn = mx2 + ve > ref + 15.f ? mx2 + ve - 11.f : ref;
+          // 2^(s + ve - R) serves the products and, times 2^(R - ve - m), the row sum
+          if (__any_sync(0xffffffffu, kf == 0.f || ve == kWide || rn - ve - mn > 90.f)) {
+            wide_tile(a, e, t, kt, sl2q, kf, ve, tS, m, l, ref, &sh.alpha[q][rl], &sh.alpha_full[q]);
+            tc_fence_before();
+            mbar_arrive(&sh.p_full[q]);
+            ++cs;
+            continue;
+          }
+          alpha = mn == -INFINITY ? 1.f : ex2(m - mn);
+          m = mn;
+          sh.alpha[q][rl] = rn == ref ? 1.f : ex2(ref - rn);       // 0 when R = -inf
+          ref = rn;
+          mneg = rn == -INFINITY ? 0.f : ve - rn;
+          lfac = m == -INFINITY ? 1.f : ex2(rn - ve - m);
         } else {
+          // m is the running max less kLift: the largest P is 2^kLift
+          const float mx2 = row_max128(s) * sl2 - kLift;
+          if (mx2 > m) {
+            alpha = ex2(m - mx2);                         // 0 when m = -inf
+            m = mx2;
+          }
           sh.alpha[q][rl] = alpha;
+          mneg = (m == -INFINITY) ? 0.f : -m;
         }
         mbar_arrive(&sh.alpha_full[q]);
-        const float mneg = (m == -INFINITY) ? 0.f : -m;
         const float2 sl2v = make_float2(sl2, sl2), mnegv = make_float2(mneg, mneg);
         float2 acc[4] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         __syncwarp();                                     // P's stores are the whole warp's: rows may have parted above
@@ -753,7 +850,7 @@ __global__ void __launch_bounds__(512, 1)
           tmem_st16(tS + 16 * h, pk);
         }
         const float2 sum = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
-        l = l * alpha + (sum.x + sum.y);
+        l = l * alpha + (kFp8 ? (sum.x + sum.y) * lfac : sum.x + sum.y);
         tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&sh.p_full[q]);
@@ -774,7 +871,9 @@ __global__ void __launch_bounds__(512, 1)
         a.meta[2 * blockIdx.x + 1] = make_int4(e.row0, 0, 0, 0);
       }
       const bool odd = e.nu > 0 && *reinterpret_cast<volatile int*>(&sh.odd[q][(nseg - 1) & 1]) == nseg;
-      const float inv = whole ? (l == 0.f ? 0.f : vref / l) : vref;
+      // E4M3: O's reference from R to m, 2^(R - m) in two steps: it may lie outside fp32's normal range
+      const float half = !kFp8 ? 1.f : ref == -INFINITY ? 0.f : ex2(0.5f * (ref - m));
+      const float inv = whole ? (l == 0.f ? 0.f : half / l) : half;
       const int hq = e.h * a.G + (R - t * a.G);
       const long long tk = e.s.cu0 + t;
       if (live) {
@@ -797,6 +896,10 @@ __global__ void __launch_bounds__(512, 1)
           for (int i = 0; i < 32; ++i) o[i] = 0u;
         }
         if (live) {
+          if constexpr (kFp8) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * half);
+          }
           if (odd) {                                      // rare: see the top of the file
             // keys of the segment's tiles that were made safe; j < 0 is the prefix
             const int j1 = min(e.s.T, (e.kt0 + e.nu) * kChunk - e.s.len);

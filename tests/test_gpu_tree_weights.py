@@ -6,13 +6,14 @@ all rows see.  Here the kernels are held to what they promise: weights keep the 
 far below the row's largest.  For each row, with p the true weights (they sum to 1), v_j = code_j * 2^e_j (e_j = 0 in
 a 16-bit cache) and sums over the visible keys only,
 
-    |dO| <= (u + 2 ds) sum p |v| + u (1 + u) |O| + w max_j(p_j 2^e_j) sum_j |code_j| + 2^-126,
+    |dO| <= (u + 2 ds) sum p |v| + u (1 + u) |O| + w max_j(p_j 2^e_j) sum_j |code_j| + 2^-126 (1 + max(p) sum |v|),
 
 u half a step of the 16-bit type, ds = 2^-16 (R + 1) the scores' error as there.  The third term: in a 16-bit cache
 P's largest is 2^15, and below 2^-14 fp16 is off by 2^-25, so w = 2^-40.  E4M3 weights p_j 2^e_j have a largest of
 2^11 at least, which gives 2^-36; 128 keys whose scales are all within 2^8 may share a reference, which then
-lies up to 2^8 above the row's own largest: w = 2^-28.  The last term is what fp32 resolves; a result below
-fp16's normal range is off by 2^-25 itself."""
+lies up to 2^8 above the row's own largest: w = 2^-28.  The last term is fp32's range: a weight below 2^-126 of the largest,
+exp(-87.3), is zero where 32-bit sums of parts of the keys are merged (the factor 2^(m_i - m) of a part underflows), so
+the key is lost with p |v| <= 2^-126 max(p) |v|; a result below fp16's normal range is off by 2^-25 itself."""
 
 from __future__ import annotations
 
@@ -29,12 +30,12 @@ BF, HF = torch.bfloat16, torch.float16
 
 
 def exact(q, k, v, see, scale, e=None):
-    """fp64 on the GPU: q [T, Hq, d], k, v [Hk, n, d], see [T, n], e [Hk, n].  O, LSE, sum p |v|, the third term's
-    max times sum, and R."""
+    """fp64 on the GPU: q [T, Hq, d], k, v [Hk, n, d], see [T, n], e [Hk, n].  O, LSE, sum p |v|, the third and the
+    last term's max times sum, and R."""
     T, Hq, d = q.shape
     G = Hq // k.shape[0]
     q = q.double()
-    o, a, low = (torch.zeros_like(q) for _ in range(3))
+    o, a, low, tiny = (torch.zeros_like(q) for _ in range(4))
     lse, r = (torch.zeros(T, Hq, dtype=torch.float64, device=q.device) for _ in range(2))
     for h in range(Hq):
         kk, vv = k[h // G].double(), v[h // G].double()
@@ -46,21 +47,22 @@ def exact(q, k, v, see, scale, e=None):
             p = torch.exp(s - lse[t, h])
             o[t, h], a[t, h] = p @ vv[i], p @ vv[i].abs()
             low[t, h] = (p * size[i]).max() * (vv[i].abs() / size[i][:, None]).sum(0)
+            tiny[t, h] = 1 + p.max() * vv[i].abs().sum(0)
             r[t, h] = (scale * (kk[i].abs() @ q[t, h].abs())).max()
-    return o, lse, a, low, r
+    return o, lse, a, low, tiny, r
 
 
 def check(q, o, lse, want, w=2.0 ** -40, label="", rows=None):
     u = float(torch.finfo(q.dtype).eps) / 2
     rows = slice(None) if rows is None else rows
     o, lse = o[rows], lse[rows]
-    ro, rl, a, low, r = (x[rows] for x in want)
+    ro, rl, a, low, tiny, r = (x[rows] for x in want)
     ds = 2.0 ** -16 * (r + 1)
     assert torch.isfinite(o).all() and torch.isfinite(lse).all(), f"{label}: not finite"
     dl = (lse.double() - rl).abs() - (ds + 2.0 ** -20 * (1 + rl.abs()))
     assert float(dl.max()) <= 0, f"{label}: lse over its bound by {float(dl.max())}"
     d = (o.double() - ro).abs()
-    bound = (u + 2 * ds[..., None]) * a + u * (1 + u) * ro.abs() + w * low + 2.0 ** -126
+    bound = (u + 2 * ds[..., None]) * a + u * (1 + u) * ro.abs() + w * low + 2.0 ** -126 * tiny
     bound = bound + (2.0 ** -25 if q.dtype is HF else 0.0)
     over = (d / bound).max()
     assert float(over) <= 1, f"{label}: {float(over)} times the bound (off by {float(d.max())})"
@@ -135,7 +137,7 @@ def _rows(N, seed, heads=2, d=64):
     return torch.randn(N, heads, d, generator=g)
 
 
-@pytest.mark.parametrize("n", [2, 8])
+@pytest.mark.parametrize("n", [2, 8, 40])
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("tree", [False, True])
 @pytest.mark.parametrize("which,up", [("v", 12), ("v", 24), ("v", 34), ("v", 60), ("v", 120), ("k", 17), ("k", 25), ("k", 40),
@@ -155,7 +157,7 @@ def test_finite_keys_a_row_does_not_see_do_not_reach_it(which, up, dtype, tree, 
     c.attend(_rows(n, 3, 4).to(dtype).cuda(), n, mask, big)
 
 
-@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("n", [1, 6, 40])
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("up", [12, 24, 40, 60])
 @pytest.mark.parametrize("where", [0, 130, 199])
@@ -170,7 +172,7 @@ def test_large_values_of_no_weight(dtype, n, up, where):
     Filled(k, v).attend(q.to(dtype).cuda(), n)
 
 
-@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("n", [1, 6, 40])
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("up", [17, 25, 40, 100])
 def test_large_keys_across_the_queries(dtype, n, up):
@@ -185,7 +187,7 @@ def test_large_keys_across_the_queries(dtype, n, up):
     Filled(k, v).attend(q.to(dtype).cuda(), n)
 
 
-@pytest.mark.parametrize("n", [1, 6])
+@pytest.mark.parametrize("n", [1, 6, 40])
 @pytest.mark.parametrize("dtype", [BF, HF])
 @pytest.mark.parametrize("step", [-30, -9, 9, 30])
 def test_values_that_grow_or_fall_along_the_keys(dtype, n, step):
@@ -203,4 +205,23 @@ def test_values_that_grow_or_fall_along_the_keys(dtype, n, step):
         kb[64 * b:64 * b + 64, :, 0] = 0.0
         if dtype is HF and step * (b - 2) > 12:
             continue                                     # not a result that fp16 holds
+        Filled(kb, v).attend(q.to(dtype).cuda(), n)
+
+
+@pytest.mark.parametrize("n", [1, 6, 40])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("step", [-100, 100])
+def test_values_far_apart_from_one_tile_to_the_next(dtype, n, step):
+    """Tiles of 128 keys, alike inside, whose values are 2^step times those of the tile before."""
+    N = 384 + n
+    k, v, q = _rows(N, 1), _rows(N, 2), _rows(n, 3, 4)
+    for b in range(3):
+        v[128 * b:128 * b + 128] *= 2.0 ** (step * (b - 1))
+    v[384:] = 0
+    k[..., 0], q[..., 0] = -100.0, 8.0
+    for b in range(3):
+        if dtype is HF and step * (b - 1) > 0:
+            continue                                     # not a result that fp16 holds
+        kb = k.clone()
+        kb[128 * b:128 * b + 128, :, 0] = 0.0
         Filled(kb, v).attend(q.to(dtype).cuda(), n)
