@@ -65,7 +65,7 @@ __device__ __forceinline__ int owner_of(const int* cu, int B, int tok) {
 // E4M3 rows.  A row of d values x is stored as codes and one power-of-two scale 2^e, with e the
 // smallest exponent for which max |x| <= 448 * 2^e: the largest magnitude lands in (224, 448], the
 // codes are x * 2^-e (an exact product) rounded to nearest even, and code * 2^e is exact in
-// bf16, so reading back adds no error.  A power of two costs no precision against max/448: E4M3
+// bf16 (from its smallest normal value up), so reading back adds no error.  A power of two costs no precision against max/448: E4M3
 // is a floating type, so a factor below 2 moves no value out of its normal range but the lowest binade.
 // ------------------------------------------------------------------------------------
 
@@ -76,7 +76,8 @@ __device__ __forceinline__ int scale_code(float amax) {
   const int s = static_cast<int>(u >> 23) - 8 + ((u & 0x7FFFFFu) > 0x600000u ? 1 : 0);
   return max(s, 1);                      // at most 254 - 8 + 1 = 247
 }
-__device__ __forceinline__ float scale_value(uint32_t code) { return __uint_as_float(code << 23); }   // 2^(code - 127)
+// 2^(code - 127), code 0 .. 254 (0: below fp32's normal range)
+__device__ __forceinline__ float scale_value(uint32_t code) { return __uint_as_float(code == 0 ? 0x400000u : code << 23); }
 __device__ __forceinline__ float scale_inverse(int code) { return __uint_as_float((254u - code) << 23); }
 
 // Two fp32 to two E4M3 codes (lo = first), round to nearest even; NaN gives the NaN code.

@@ -393,7 +393,8 @@ int fa_fwd_fp8(const fa_fwd_fp8_args* args);
  * page_size], h].  Sequences may share pages that are only read.  Element types:
  *   FA_BF16, FA_FP16 : the rows as they are;
  *   FA_E4M3          : E4M3 codes and, for each row of d values, one E8M0 scale code (1 .. 247
- *                      as fa_cache_append writes them), value = code * 2^(scale - 127).
+ *                      as fa_cache_append writes them; any from 0 to 254 may be held),
+ *                      value = code * 2^(scale - 127).
  * The lengths live on the device (lens[b]: positions held, cu_new[b] .. cu_new[b + 1]: the new
  * tokens of sequence b among the call's `total`), so a captured graph can be replayed with other
  * lengths.  What the host cannot see is checked by the kernels: a negative length, a position
@@ -445,7 +446,7 @@ int fa_cache_append(const fa_cache_append_args* args);
 
 /*
  * Read the cache back: k_out, v_out [B, Hk, N, d] of dtype (the cache's, or FA_BF16 or FA_FP16 of
- * an E4M3 cache, each value rounded to nearest: exact in bf16), rows n < lens[b] of each sequence
+ * an E4M3 cache, each value rounded to nearest: exact in bf16 from 2^-126 up), rows n < lens[b] of each sequence
  * and zeros from there to N.  The layout is that of fa_fwd_partial's keys.  One launch.
  */
 typedef struct {

@@ -237,3 +237,25 @@ def test_append_reports_bounds_that_cannot_be(fp8):
     some = torch.tensor([1, 2, 3, 3], dtype=torch.int32).cuda()
     fa.cache_append(c.cache, gk, gv, some, c.lens)
     fa.fa_check_status()
+
+
+@pytest.mark.parametrize("out", [BF, HF])
+def test_every_code_and_scale_is_read_as_what_it_stands_for(out):
+    """All 256 codes under all scale codes from 0 (2^-127) to 254."""
+    d, page = 64, 128
+    codes = torch.arange(256, dtype=torch.uint8).view(4, d).repeat(255, 1).cuda()          # row 4 s + i: scale s
+    scales = torch.arange(255, dtype=torch.uint8).repeat_interleave(4).cuda()
+    N = codes.shape[0]
+    pages = -(-N // page)
+    k = torch.zeros(pages, 1, page, d, dtype=torch.uint8, device="cuda")
+    ks = torch.zeros(pages, 1, page, dtype=torch.uint8, device="cuda")
+    k.view(-1, d)[:N], ks.view(-1)[:N] = codes, scales
+    cache = fa.KVCache(k, k.clone(), torch.arange(pages, dtype=torch.int32, device="cuda")[None], ks, ks.clone())
+    got = fa.cache_read(cache, torch.tensor([N], dtype=torch.int32, device="cuda"), N, dtype=out)
+    fa.fa_check_status()
+    want = ora.e4m3_values(codes.cpu().numpy()) * np.exp2(scales.cpu().numpy().astype(np.float64) - 127)[:, None]
+    want = torch.from_numpy(want).to(out)
+    for x in got:
+        x = x.cpu()[0, 0]
+        assert torch.equal(torch.isnan(x), torch.isnan(want))
+        assert torch.equal(torch.nan_to_num(x, nan=0.0), torch.nan_to_num(want, nan=0.0))
