@@ -828,6 +828,14 @@ int most_rows(int total, int G) {
   return (int)(r < kBigRows ? r : kBigRows);
 }
 
+// Whether the rows of d values of an [n0, n1, d] tensor of these strides lie apart.
+bool rows_apart(long long n0, long long s0, long long n1, long long s1, int d) {
+  if (n0 <= 1) s0 = LLONG_MAX;
+  if (n1 <= 1) s1 = LLONG_MAX;
+  const long long lo = s0 < s1 ? s0 : s1, hi = s0 < s1 ? s1 : s0, n = s0 < s1 ? n0 : n1;
+  return lo >= d && (hi == LLONG_MAX || (hi - d) / lo >= n - 1);
+}
+
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 }  // namespace
@@ -860,6 +868,7 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   for (const long long s : {(long long)x.q_token_stride, (long long)x.q_head_stride, (long long)x.o_token_stride,
                             (long long)x.o_head_stride})
     if (s < 0 || s % 8 != 0) return FA_ERR_INVALID_ARG;
+  if (!rows_apart(x.total, x.o_token_stride, x.Hq, x.o_head_stride, x.cache.d)) return FA_ERR_INVALID_ARG;
   const int G = x.Hq / x.cache.Hk;
   if ((long long)x.max_new * G > INT_MAX - 256) return FA_ERR_UNSUPPORTED;
   const TreeLayout w = tree_layout(most_rows(x.total, G), x.cache.d);

@@ -488,7 +488,7 @@ int fa_cache_keep(const fa_cache_keep_args* args);
  *                    (cu_new[b] + t)'s row: whether it sees new token j of its sequence (itself
  *                    included: nothing is seen that has no bit)
  *   q       : in,  [total, Hq, d] (dtype), strides in elements, multiples of 8
- *   o       : out, [total, Hq, d] (dtype), strides likewise; lse : out, fp32 [total, Hq], dense
+ *   o       : out, [total, Hq, d] (dtype), strides likewise, rows that do not overlap; lse : out, fp32 [total, Hq], dense
  *   max_new : at least every sequence's number of new tokens (a sequence with more is reported
  *             as FA_ERR_RANGE); it and Hq / Hk choose the kernel.  0 says that no sequence has
  *             any (all of the call's tokens are padding): nothing is written, and with workspace
