@@ -39,8 +39,8 @@ __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
 
 // Eight 16-bit values of a row to eight E4M3 codes; the row is spread over kLanes lanes.  Magnitudes
 // are compared as 16-bit integers (the order of the bits is the order of the values, infinities and NaN
-// last), two at a time: the arithmetic, not HBM, bounds a prompt's append when every value is checked
-// and compared in 32 bits (16384 tokens of 8 heads of 128: 25 us).
+// last), two at a time (every value checked and compared in 32 bits: 25 us for what takes 19 now, 14.8k tokens
+// of 8 heads of 128).  The arithmetic still takes longer than the bytes: widening, scaling and conversion of each value.
 template <bool kFp16, int kLanes>
 __device__ __forceinline__ uint2 quantise8(const uint4& w, int& code) {
   // A magnitude that E4M3 would round up past the source type's largest value is taken down to
@@ -140,8 +140,10 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendArgs a) {
 
 template <int D, bool kFp8, bool kFp16>
 cudaError_t launch_append(const AppendArgs& a, unsigned blocks, int steps, cudaStream_t s) {
-  return steps == 4 ? launch_after(append_kernel<D, kFp8, kFp16, 4>, dim3(blocks), 256, 0, s, a)
-                    : launch_after(append_kernel<D, kFp8, kFp16, 1>, dim3(blocks), 256, 0, s, a);
+  if constexpr (kFp8) {
+    if (steps == 4) return launch_after(append_kernel<D, kFp8, kFp16, 4>, dim3(blocks), 256, 0, s, a);
+  }
+  return launch_after(append_kernel<D, kFp8, kFp16, 1>, dim3(blocks), 256, 0, s, a);
 }
 
 // ------------------------------------------------------------------------------------
@@ -338,9 +340,13 @@ int fa_cache_append(const fa_cache_append_args* p) {
     return FA_ERR_INVALID_ARG;
   AppendArgs a{};
   int heads = 32 / (x.cache.d / 8);
-  // Prompts: four steps a warp, so that the lookup is paid for 4 KB instead of 1 KB (16384 tokens of 8
-  // heads of 128 into E4M3: 28 us with one, 25 with four).  A decoding step: more warps with one step each.
-  const int steps = (long long)x.total * x.cache.Hk >= 148 * 64 * heads && x.cache.Hk >= 2 * heads ? 4 : 1;
+  // A prompt into E4M3: four steps a warp, so that the lookup is paid for 4 KB instead of 1 KB, where three quarters of
+  // the steps have a head.  Four against one, us: 16384 tokens of 8 heads of 128 23.9 : 27.3, of 6 (three of four)
+  // 21.9 : 21.9, twice as many 36.2 : 38.2; of 4 (two of four) 19.8 : 16.4; 4096 tokens of 8 10.9 : 10.2.  A 16-bit cache
+  // (no arithmetic) takes the same time either way, within 3 %.
+  const bool fp8 = x.cache.dtype == FA_E4M3;
+  const int one = (x.cache.Hk + heads - 1) / heads, four = (one + 3) / 4;      // steps for all heads; warps of four
+  const int steps = fp8 && (long long)x.total * x.cache.Hk * x.cache.d >= 3LL << 22 && 4LL * one >= 12LL * four ? 4 : 1;
   heads *= steps;
   a.groups = (x.cache.Hk + heads - 1) / heads;
   const long long blocks = ((long long)x.total * a.groups + 7) / 8;
@@ -355,7 +361,7 @@ int fa_cache_append(const fa_cache_append_args* p) {
   a.lens = x.lens;
   a.total = x.total;
   const cudaStream_t s = static_cast<cudaStream_t>(x.stream);
-  const bool fp8 = x.cache.dtype == FA_E4M3, fp16 = x.dtype == FA_FP16;
+  const bool fp16 = x.dtype == FA_FP16;
   const unsigned g = (unsigned)blocks;
   return launched([&]() -> cudaError_t {
     if (x.cache.d == 128) {

@@ -57,7 +57,7 @@ def _held(cache, x, b, n):
 def test_prompts_are_appended(d, Hk, dtype, fp8):
     """Calls about the size from which a warp takes four groups of heads, on both sides of it, with key heads that do
     not fill the last group."""
-    edge = -(-148 * 64 * (256 // d) // Hk)               # tokens
+    edge = -(-3 * 2 ** 22 // (Hk * d))                   # tokens
     g = torch.Generator(device="cuda").manual_seed(Hk)
     for total in (edge - 1, edge, edge + 777):
         counts = [total // 3, 0, total - total // 3]
