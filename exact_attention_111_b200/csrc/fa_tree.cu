@@ -14,11 +14,14 @@
 // eight are merged through shared memory.  (With a ring of its own for each warp, filled by the warp, the
 // copies' issue took 700 of a step's 2000 cycles; a ninth warp filling the eight rings was the bottleneck.)
 //
-// Measured: a decoding step of 64 sequences of 1024 to 8191 keys, 32 query and 8 key heads of 128, bf16: 177
-// us, 6.3 TB/s of the cache's bytes (98 % of the copy rate, DRAM 77 % busy by its own count).  One token over
-// 131072 E4M3 keys, 32 query and 4 key heads of 128: 35 us against 21 of bytes; a step of 32 keys takes
-// some 2100 cycles of dependent loads, conversions, products and exponentials on two warps a scheduler,
-// and 4 us go into the start and the merges.  One token of 1023 keys, 16 heads of 64: 7.7 us, all latency.
+// Measured (captured graphs, in bursts): a decoding step of 64 sequences of 1024 to 8191 keys, 32 query and 8 key
+// heads of 128, bf16: 177 us, 6.3 TB/s of the cache's bytes (98 % of the copy rate, DRAM 77 % busy by its own
+// count); 3 of them are the merge kernel's.  One token over 131072 E4M3 keys, 32 query and 4 key heads of 128: 35 us
+// against 21 of bytes; 3 for the merge, and of the 31 of a CTA (58000 cycles) 17 for the fourteen steps of a warp (2280
+// cycles each of dependent loads, conversions, products and exponentials, on two warps a scheduler), 7 waiting
+// for keys, 6 until the first ones are there.
+// One token of 1023 keys, 16 heads of 64: 7.7 us, all latency: 2 until a CTA knows its part, 2 for its
+// one chunk, 1 to use and sum it, 1.6 for the merge, the rest between launches.
 //
 // The products are made transposed, S^T = K Q^T and O^T = V^T P^T (mma.sync m16n8k16): keys and columns
 // fill the 16-wide side and rows come in eights, so four or eight query heads of a group cost
@@ -789,9 +792,10 @@ cudaError_t launch_small(const CUtensorMap& tk, const CUtensorMap& tv, const Tre
 
 template <int D, bool kFp8, bool kFp16>
 cudaError_t launch_small_nr(const CUtensorMap& tk, const CUtensorMap& tv, const TreeArgs& a, int ctas, cudaStream_t s) {
-  return a.tile_rows == 8    ? launch_small<D, kFp8, kFp16, 1>(tk, tv, a, ctas, s)
-         : a.tile_rows == 16 ? launch_small<D, kFp8, kFp16, 2>(tk, tv, a, ctas, s)
-                             : launch_small<D, kFp8, kFp16, 4>(tk, tv, a, ctas, s);
+  if constexpr (D == 64) {                                 // (most_small)
+    if (a.tile_rows == 32) return launch_small<D, kFp8, kFp16, 4>(tk, tv, a, ctas, s);
+  }
+  return a.tile_rows == 8 ? launch_small<D, kFp8, kFp16, 1>(tk, tv, a, ctas, s) : launch_small<D, kFp8, kFp16, 2>(tk, tv, a, ctas, s);
 }
 
 template <int D>
@@ -821,6 +825,12 @@ TreeLayout tree_layout(int rows, int d) {
   w.total = w.meta + up((size_t)kTreeCtas * 2 * sizeof(int4));
   return w;
 }
+
+// Most rows of a key head that the few-row kernel takes.  At d = 64 it takes up to 32: 32 sequences of up to 8191 keys,
+// 8 key heads, 20 rows 123 us against 141 of the many-row kernel (16 bits) and 135 against 198 (E4M3), 32 rows 107
+// against 128 and 117 against 176.  At d = 128 four row blocks spill: 20 rows 305 against 165 (16 bits) and 319 against
+// 227 (E4M3), 32 rows 274 against 148 and 272 against 201; up to 16 it is ahead, 123 against 148 and 108 against 211.
+int most_small(int d) { return d == 64 ? 32 : 16; }
 
 // Most rows a row tile can have in a call with this many new tokens.
 int most_rows(int total, int G) {
@@ -898,7 +908,7 @@ int fa_fwd_tree(const fa_fwd_tree_args* p) {
   a.timeout_ns = 2000000000ull;
   a.scale_log2 = (float)((double)x.scale * 1.4426950408889634);
   const long long unit = (long long)min(x.max_new, x.total) * G;   // most rows of a key head
-  const bool big = unit > 32;
+  const bool big = unit > most_small(x.cache.d);
   a.tile_rows = big ? kBigRows : unit <= 8 ? 8 : unit <= 16 ? 16 : 32;
   a.slot_rows = min(a.tile_rows, most_rows(x.total, G));
   a.chunk_shift = !big && x.cache.d * (fp8 ? 1 : 2) <= 128 ? 8 : 7;   // 32-key steps: SmallCfg
