@@ -15,13 +15,18 @@
 //
 // Why two query tiles: K and V come from L2 or HBM once for 256 rows, and one tile's softmax runs beside the
 // other's products.  What bounds it: per 128 keys 2048 cycles of MMA and 2048 of exponentials (16 a clock);
-// a tile pair takes about 3100 cycles at 16 bits (softmax 1850, then 1200 until the next S: P V and S
+// a tile pair takes 3550 to 3750 at 16 bits (softmax 1850 to 2000, then 1700 to 1750 until the next S: P V and S
 // behind the other tile's).  Issue matters: the MMA warp walks converged with its operands in uniform
-// registers (trees of 64 tokens 162 -> 156 us).  E4M3: about 5700 cycles; K's staging and expansion (3200 +
-// 2700 cycles, one buffer: shared memory is full at d = 128) set the pace.  Measured in bursts (at sustained
-// load the clock falls and the first takes 184 us): 8 trees of up to 64 tokens over up to 16384 keys, 64
-// query and 8 key heads of 128, bf16: 158 us, 695 TFLOP/s; 2 chunks of 512 over 16000 keys, 32 and 8 heads,
-// fp16: 137 us, 758 TFLOP/s; 16 trees of up to 48 over up to 8000 E4M3 keys: 151 us, 352 TFLOP/s.
+// registers (trees of 64 tokens 162 -> 156 us).  E4M3: 5300 to 5600 cycles (softmax 3000 to 3400 beside the
+// expansions' issue, then 2250); K's staging and expansion, one after the other in one buffer (shared memory is full
+// at d = 128), set the pace.
+//
+// Measured in captured graphs in bursts (at sustained load the clock falls: 185, 153 and 149 us): 8 trees of up to 64
+// tokens over up to 16384 keys, 64 query and 8 key heads of 128, bf16: 157 us, 699 TFLOP/s; 2 chunks of 512 over 16000
+// keys, 32 and 8 heads, fp16: 137 us, 760 TFLOP/s; 16 trees of up to 48 over up to 8000 E4M3 keys: 147 us, 361 TFLOP/s.
+// Where the first's go: 9 to the merge kernel; the slowest CTA takes 1.16 times the median one (the parts are equal
+// in chunks, not in rows: chunks 1.25, E4M3 trees 1.18), and the median one's 233000 cycles at 1.73 GHz are 206000 for
+// 59 tiles, 15000 for Q and the first S of its segments, 12000 for their results, 2000 to find its part.
 //
 // A masked product is 0 * v, which is not 0 where v is not finite.  Tiles that hold new tokens (which some
 // rows see and others do not) or reach past the end are therefore read once more by the correction
