@@ -225,3 +225,20 @@ def test_values_far_apart_from_one_tile_to_the_next(dtype, n, step):
         kb = k.clone()
         kb[128 * b:128 * b + 128, :, 0] = 0.0
         Filled(kb, v).attend(q.to(dtype).cuda(), n)
+
+
+@pytest.mark.parametrize("n", [8, 40])
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("N0", [0, 120, 200])
+def test_unseen_keys_of_any_size_beside_some_that_are_not_finite(N0, dtype, n):
+    """Siblings whose rows are NaN, infinite or 2^60 as large, in one tile."""
+    N = N0 + n
+    k, v = _rows(N, 1), _rows(N, 2)
+    odd = [1, 2, 4, 5, 6]
+    v[N0 + 1] = float("nan")
+    v[N0 + 2] *= 2.0 ** 60
+    k[N0 + 4] *= 2.0 ** 60
+    k[N0 + 5, :, ::3] = float("nan")
+    v[N0 + 6, :, 7] = float("inf")
+    mask = fa.tree_mask([-1] + [0] * (n - 1), torch.tensor([0, n], device="cuda"))
+    Filled(k, v).attend(_rows(n, 3, 4).to(dtype).cuda(), n, mask, odd)
