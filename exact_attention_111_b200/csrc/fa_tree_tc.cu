@@ -111,8 +111,8 @@ struct BigShared {
   // publishes after it has read entry n.
   int odd[2][2];
   float alpha[2][kTile];
-  // E4M3: staged scale codes of a tile (K's and V's with K, V's with V), and by tile mod 8 2^E of its K and E of its V
-  // (kfac 0, vexp kWide: rows as they are).  Entry u is written again for tile u + 8, whose K slot is free only
+  // E4M3: staged scale codes of a tile (K's and V's with K, V's with V), and by tile mod 8 2^E of its K and
+  // E of its V (kfac 0, vexp kWide: rows as they are).  Entry u is written again for tile u + 8, whose K slot is free only
   // after S of tile u + 8 - kStages, so of u + 4, which waited for both softmax groups to have finished u + 3.
   alignas(16) uint8_t scales[3][kTile];
   float kfac[8], vexp[8];
@@ -128,9 +128,9 @@ __device__ __forceinline__ bool tail_tile(const Seg& e, int kt) { return (kt + 1
 // reference R of each row's own, which follows the largest max(s) + E of the row's tiles (visible keys only): R is
 // moved (and O with it) when one is 2^15 above it, to 2^11 under it.  Weights keep fp16's eleven bits down to 2^-25
 // of the row's largest, or 2^-17 where a tile puts R too high by a key of up to 2^8 the size that the row
-// does not see.  A tile whose scales are further apart ("wide") keeps its rows as they are, and the softmax takes each key's scale
-// from the cache, K's to the score and V's to the weight, so that no key's size depends on another's.
-// Rows of scale code 0 or 1 (zeros, and values below 2^-117) do not make a tile wide; they become zero beside
+// does not see.  A tile whose scales are further apart ("wide") keeps its rows as they are, and the softmax takes
+// each key's scale from the cache, K's to the score and V's to the weight, so that no key's size depends on
+// another's.  Rows of scale code 0 or 1 (zeros, and values below 2^-117) do not make a tile wide; they become zero beside
 // others 2^25 as large.
 //
 // Warp 12 keeps one tile's codes of K and of V ahead in shared memory by TMA.  Warps 14 and 15 expand
